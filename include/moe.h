@@ -261,6 +261,136 @@ int moe_layer_forward_static(const void *x, const float *router_w, const float *
  * Allocates nothing. */
 int moe_layer_forward_static_check(void *stream);
 
+/*
+ * The attention half of a decoder block between its projections, for callers that run one next
+ * to the routed layer: norms and rotation of q and k with the append to a paged cache, attention
+ * of one new token per sequence over that cache, and copies and moves of its pages.
+ *
+ * Conventions of these entry points where they differ from the ones above:
+ *  - they need no moe_init and allocate nothing; they run on the device that is current, and all
+ *    pointers must belong to it. The first call on a device looks up its error word;
+ *  - calls on several streams or host threads may overlap, as long as no call writes what
+ *    another reads or writes (a workspace is written);
+ *  - what the kernels find wrong in device data (a page, length or slot out of range) is never
+ *    followed: the access is skipped, recorded in the device's error word, and reported by the
+ *    next moe_cache_check on that device.
+ */
+#define MOE_DT_BF16 0
+#define MOE_DT_F16 1
+#define MOE_DT_E4M3 2   /* 8-bit floats of 4 exponent and 3 mantissa bits; caches only */
+
+/*
+ * A cache of keys and values in pages of page_size tokens. Element (page, token, head, i) of
+ * layer l lies at k + l * layer_stride + page * page_stride + token * token_stride +
+ * head * head_stride + i, in elements; v has the same strides. Any order of the dimensions
+ * and any gaps are fine, as long as no two elements share a place, every row of head_dim
+ * elements is contiguous, and the bases and strides are multiples of 16 bytes.
+ * A stored value stands for value * k_scale (v_scale); both are 1 unless dtype is MOE_DT_E4M3.
+ */
+typedef struct moe_kv_cache {
+  void *k, *v;
+  int dtype;                      /* MOE_DT_* */
+  int n_layers, num_pages, page_size, n_kv;
+  int head_dim;                   /* a multiple of 16, at most 512 */
+  long long layer_stride, page_stride, token_stride, head_stride;
+  float k_scale, v_scale;         /* > 0 */
+} moe_kv_cache;
+
+/* Rows of heads: element (t, h, i) at p + t * token_stride + h * head_stride + i (elements; p
+ * and the strides multiples of 16 bytes). */
+typedef struct moe_heads {
+  void *p;
+  long long token_stride, head_stride;
+} moe_heads;
+
+/*
+ * moe_qk_norm_rope: for T tokens, the per-head norms of q and k, their rotation, and the append
+ * of k and v to a cache, in one pass:
+ *   u = x / sqrt(mean_i x_i^2 + eps) * gain   (FP32; with a null gain u = x)
+ *   pairs (u_a, u_b) turn by positions[t] * inv_freq[i] (64-bit angles), i < rotary_dim / 2:
+ *   y_a = rope_scale (u_a cos - u_b sin),  y_b = rope_scale (u_b cos + u_a sin)
+ *   half layout: (a, b) = (i, i + rotary_dim / 2); interleaved: (2 i, 2 i + 1). Elements from
+ *   rotary_dim on keep u.
+ *   q, k, v     [T, n_q | n_kv, head_dim] of type dtype (MOE_DT_BF16 or MOE_DT_F16); n_q or n_kv
+ *               may be 0; v is read only for the cache
+ *   positions   device int32 [T];  inv_freq device float64 [rotary_dim / 2]
+ *   rotary_dim  0 (no rotation; positions and inv_freq may be NULL) to head_dim: a multiple of
+ *               16 in the half layout, even when interleaved
+ *   q_gain, k_gain  device fp32 [head_dim], 16-byte aligned, or NULL for no norm
+ *   q_out, k_out    where rotated q and k go, type dtype; NULL leaves k_out out (q_out only
+ *               where n_q = 0). Each may be its own input (same base and strides).
+ *   cache, layer, slots  NULL, or the cache that k (rotated) and v are stored in: token t in row
+ *               slots[t] % page_size of page slots[t] / page_size (device int64 [T]; negative:
+ *               not stored). Its dtype is dtype or MOE_DT_E4M3 (value / scale, saturated at
+ *               +-448). Slots that are not negative must be distinct: of tokens with the same
+ *               slot, which one's values remain is not defined.
+ * Sums and products in FP32, rounded once. T = 0 is a no-op.
+ */
+int moe_qk_norm_rope(const moe_heads *q, const moe_heads *k, const moe_heads *v, int dtype, int T, int n_q,
+                     int n_kv, int head_dim, const int32_t *positions, const double *inv_freq, int rotary_dim,
+                     int interleaved, float rope_scale, const float *q_gain, const float *k_gain, float eps,
+                     const moe_heads *q_out, const moe_heads *k_out, const moe_kv_cache *cache, int layer,
+                     const int64_t *slots, void *stream);
+
+/*
+ * moe_rope_frequencies: host function; fills inv_freq (host, [rotary_dim / 2]) and *rope_scale.
+ *   MOE_ROPE_PLAIN   base^(-2 i / rotary_dim)
+ *   MOE_ROPE_LINEAR  the same over factor (positions interpolated)
+ *   MOE_ROPE_NTK     base replaced by base * factor^(rotary_dim / (rotary_dim - 2))
+ *   MOE_ROPE_YARN    (YaRN, arXiv 2309.00071) a pair that makes more than beta_fast turns in
+ *                    original_length tokens keeps its frequency, one that makes fewer than
+ *                    beta_slow is interpolated, those between are blended linearly in i;
+ *                    *rope_scale = 0.1 ln(factor) + 1 (1 for the other kinds)
+ * factor >= 1. original_length and the betas are read by MOE_ROPE_YARN only.
+ */
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_NTK 2
+#define MOE_ROPE_YARN 3
+int moe_rope_frequencies(int kind, int rotary_dim, double base, double factor, double original_length,
+                         double beta_fast, double beta_slow, double *inv_freq, float *rope_scale);
+
+/*
+ * moe_attention_decode: attention of one new token per sequence over its cached keys, the new
+ * token's own among them:
+ *   s_j = scale * q . k_j,  j in [max(0, len - window), len)  (window 0: all of [0, len))
+ *   out = sum_j softmax(s)_j v_j;  lse = log sum_j exp(s_j)
+ *   q            [B, n_q, head_dim], dtype MOE_DT_BF16 or MOE_DT_F16, equal to the cache's unless
+ *                that is MOE_DT_E4M3; query head h reads KV head h / (n_q / n_kv)
+ *   block_tables device int32 [B, max_pages], rows table_stride apart: page of tokens
+ *                i * page_size ... of a sequence. Entries past a sequence's end are not read.
+ *   seq_lens     device int32 [B], keys per sequence. Length 0, and a sequence whose scores are
+ *                all -inf, gives a row of zeros and lse = -inf.
+ *   out          [B, n_q, head_dim] of q's type;  lse device fp32 [B, n_q] or NULL
+ *   workspace    device, moe_attention_decode_workspace_bytes(...) bytes, 16-byte aligned; needs no
+ *                initial contents and keeps nothing between calls
+ * Limits: max_pages * page_size <= 2^30. Two launches on `stream`. Deterministic: the work split
+ * follows from the lengths alone and pieces are summed in order. Softmax in FP32; the
+ * probabilities are rounded to 16 bits (bf16 for a bf16 cache, else fp16) for the product with v.
+ */
+int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cache, int layer,
+                         const int32_t *block_tables, long long table_stride, int max_pages,
+                         const int32_t *seq_lens, int B, int n_q, float scale, int window, const moe_heads *out,
+                         float *lse, void *workspace, size_t workspace_bytes, void *stream);
+/* Workspace of moe_attention_decode; 0 for a shape that it refuses. It depends on the shape of
+ * the heads alone, not on the batch or the lengths. */
+size_t moe_attention_decode_workspace_bytes(int n_q, int n_kv, int head_dim);
+
+/*
+ * moe_copy_pages: page dst[i] = page src[i] of K and V in every layer of the cache, i < n.
+ *   src, dst      HOST int32 [n]; read during the call. No page may be in dst twice or be both in
+ *                 src and in dst (MOE_ERR_BAD_ARG); src may hold a page several times (a fork).
+ *   block_tables  NULL, or device int32 [rows, cols], rows table_stride apart: a move -- every
+ *                 entry equal to src[i] becomes dst[i] in the same launch (src then distinct).
+ * n = 0 is a no-op. Under stream capture the lists become part of the graph.
+ */
+int moe_copy_pages(const moe_kv_cache *cache, const int32_t *src, const int32_t *dst, int n,
+                   int32_t *block_tables, long long table_stride, int rows, int cols, void *stream);
+
+/* moe_cache_check: synchronise `stream`, then read and clear the current device's error word:
+ * MOE_ERR_BAD_ARG if a call since the last check met a page, length or slot out of range. */
+int moe_cache_check(void *stream);
+
 /* moe_workspace_bytes: device bytes moe_init would allocate for the given limits. */
 size_t moe_workspace_bytes(int max_tokens, int max_d, int max_f, int max_E, int max_k);
 

@@ -12,5 +12,7 @@ from ._lib import (  # noqa: F401
     moe_profile_end, PROF_GROUPS, EXPORTED, moe_layer_forward_static, moe_profile_kernel_launches,
     moe_layer_forward_static_check, moe_debug_set_wait_ns, moe_debug_inject, MOE_INJECT_NONE,
     MOE_INJECT_SKIP_ROUTER_ARRIVAL, moe_block_forward, moe_route, moe_experts_forward, moe_gather_rows,
-    moe_combine_slots,
+    moe_combine_slots, MOE_DT_BF16, MOE_DT_F16, MOE_DT_E4M3, MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_NTK,
+    MOE_ROPE_YARN, MoeKvCache, moe_qk_norm_rope, moe_rope_frequencies, moe_attention_decode,
+    moe_attention_decode_workspace_bytes, moe_copy_pages, moe_cache_check,
 )

@@ -32,10 +32,18 @@ EXPORTED = (
     "moe_debug_check", "moe_workspace_bytes", "moe_profile_begin", "moe_profile_end",
     "moe_layer_forward_static", "moe_profile_kernel_launches", "moe_layer_forward_static_check",
     "moe_debug_set_wait_ns", "moe_debug_inject", "moe_block_forward", "moe_route", "moe_experts_forward",
-    "moe_gather_rows", "moe_combine_slots",
+    "moe_gather_rows", "moe_combine_slots", "moe_qk_norm_rope", "moe_rope_frequencies", "moe_attention_decode",
+    "moe_attention_decode_workspace_bytes", "moe_copy_pages", "moe_cache_check",
 )
 MOE_INJECT_NONE = 0
 MOE_INJECT_SKIP_ROUTER_ARRIVAL = 1
+MOE_DT_BF16 = 0
+MOE_DT_F16 = 1
+MOE_DT_E4M3 = 2
+MOE_ROPE_PLAIN = 0
+MOE_ROPE_LINEAR = 1
+MOE_ROPE_NTK = 2
+MOE_ROPE_YARN = 3
 PROF_GROUPS = ("route", "gateup_gemv", "down_gemv", "gateup_gemm", "down_gemm", "combine", "rmsnorm",
                "fused_decode")
 
@@ -49,6 +57,21 @@ class MoeError(RuntimeError):
 _lib = None
 _p = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
+_f = ctypes.c_float
+_d = ctypes.c_double
+
+
+class _KvCacheStruct(ctypes.Structure):
+    """moe_kv_cache"""
+    _fields_ = [("k", _p), ("v", _p), ("dtype", _i), ("n_layers", _i), ("num_pages", _i), ("page_size", _i),
+                ("n_kv", _i), ("head_dim", _i), ("layer_stride", _ll), ("page_stride", _ll), ("token_stride", _ll),
+                ("head_stride", _ll), ("k_scale", _f), ("v_scale", _f)]
+
+
+class _HeadsStruct(ctypes.Structure):
+    """moe_heads"""
+    _fields_ = [("p", _p), ("token_stride", _ll), ("head_stride", _ll)]
 
 
 def lib():
@@ -104,6 +127,20 @@ def lib():
         L.moe_debug_inject.restype = _i
         L.moe_profile_kernel_launches.argtypes = []
         L.moe_profile_kernel_launches.restype = ctypes.c_longlong
+        L.moe_qk_norm_rope.argtypes = [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _i, _i, _f, _p, _p, _f, _p, _p, _p,
+                                       _i, _p, _p]
+        L.moe_qk_norm_rope.restype = _i
+        L.moe_rope_frequencies.argtypes = [_i, _i, _d, _d, _d, _d, _d, _p, _p]
+        L.moe_rope_frequencies.restype = _i
+        L.moe_attention_decode.argtypes = [_p, _i, _p, _i, _p, _ll, _i, _p, _i, _i, _f, _i, _p, _p, _p,
+                                           ctypes.c_size_t, _p]
+        L.moe_attention_decode.restype = _i
+        L.moe_attention_decode_workspace_bytes.argtypes = [_i, _i, _i]
+        L.moe_attention_decode_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_copy_pages.argtypes = [_p, _p, _p, _i, _p, _ll, _i, _i, _p]
+        L.moe_copy_pages.restype = _i
+        L.moe_cache_check.argtypes = [_p]
+        L.moe_cache_check.restype = _i
         L.moe_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
         L.moe_workspace_bytes.restype = ctypes.c_size_t
         _lib = L
@@ -255,3 +292,222 @@ def moe_debug_set_wait_ns(ns: int) -> None:
 
 def moe_debug_inject(fault: int) -> None:
     _check(lib().moe_debug_inject(int(fault)))
+
+
+# ---------------------------------------------------------------- attention beside the layer
+#
+# These take torch tensors with their shapes and strides (the C entries take pointers and
+# strides), run on the tensors' device whichever device is current, and check here what the
+# library cannot see: types, devices and sizes.
+
+def _refuse(msg: str):
+    raise MoeError(MOE_ERR_BAD_ARG, msg)
+
+
+def _dtype_code(t) -> int:
+    import torch
+    code = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float8_e4m3fn: MOE_DT_E4M3}.get(t.dtype)
+    if code is None:
+        _refuse(f"{t.dtype} is neither bf16, fp16 nor e4m3")
+    return code
+
+
+def _need(t, name, dtype, shape, device, dense=True):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or (dense and not t.is_contiguous()):
+        _refuse(f"{name}: need a {'contiguous ' if dense else ''}{dtype} tensor of shape {tuple(shape)} on {device}, "
+                f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _heads(t, name, shape, dtype, device):
+    """moe_heads of a [T, heads, head_dim] tensor."""
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+        _refuse(f"{name}: need {dtype} {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    st = t.stride()
+    if st[2] != 1:
+        _refuse(f"{name}: the elements of a head must be contiguous")
+    return _HeadsStruct(t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current; stream None: its current stream."""
+    import torch
+    if device.type != "cuda":
+        _refuse(f"tensors must be on a CUDA device, not {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream))
+
+
+class MoeKvCache:
+    """A paged cache of keys and values over two tensors of the caller's (kept alive here):
+    layout "NHD": [pages, page_size, n_kv, head_dim]; "HND": [pages, n_kv, page_size, head_dim]; with a
+    leading dimension of layers where one tensor holds several. Any strides; bf16, fp16 or
+    float8_e4m3fn (a stored value stands for value * scale)."""
+
+    def __init__(self, k, v, layout: str = "NHD", k_scale: float = 1.0, v_scale: float = 1.0):
+        if layout not in ("NHD", "HND"):
+            _refuse(f"unknown layout {layout!r}")
+        shape, st = k.shape, k.stride()
+        if len(shape) == 4:
+            shape, st = (1,) + tuple(shape), (0,) + st
+        if len(shape) != 5 or v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype or v.device != k.device:
+            _refuse("k and v need the same shape, [(layers,) pages, ...], strides, type and device")
+        if st[4] != 1 and shape[4] > 1:
+            _refuse("the elements of a head must be contiguous")
+        token, head = (2, 3) if layout == "NHD" else (3, 2)
+        self.k, self.v, self.layout, self.device, self.dtype = k, v, layout, k.device, k.dtype
+        self.n_layers, self.num_pages, self.page_size = shape[0], shape[1], shape[token]
+        self.n_kv, self.head_dim = shape[head], shape[4]
+        st = [s if n > 1 else 0 for s, n in zip(st, shape)]
+        self.struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _dtype_code(k), shape[0], shape[1], shape[token],
+                                     shape[head], shape[4], st[0], st[1], st[token], st[head], k_scale, v_scale)
+        self.ref = ctypes.byref(self.struct)
+
+
+def moe_qk_norm_rope(q, k, v, positions, inv_freq, q_gain=None, k_gain=None, eps: float = 1e-6,
+                     interleaved: bool = False, rope_scale: float = 1.0, q_out=None, k_out=None, cache=None,
+                     layer: int = 0, slots=None, stream=None) -> None:
+    """Norms of q [T, n_q, D] and k [T, n_kv, D] per head, rotation by positions (int32 [T]) and inv_freq
+    (float64 [rotary_dim / 2], None: no rotation), into q_out and k_out and, with v, into `cache` at
+    slots (int64 [T], negative: not stored). q or k may be None."""
+    import torch
+    some = q if q is not None else k
+    if some is None or some.dim() != 3:
+        _refuse("q or k of shape [T, heads, head_dim] needed")
+    T, _, D = some.shape
+    dev, dt = some.device, some.dtype
+    refs = []
+
+    def heads(t, name, n):
+        if t is None:
+            refs.append(None)
+        else:
+            refs.append(ctypes.byref(_heads(t, name, (T, n, D), dt, dev)))
+
+    n_q = 0 if q is None else q.shape[1]
+    n_kv = 0 if k is None or k.dim() != 3 else k.shape[1]
+    heads(q, "q", n_q)
+    heads(k, "k", n_kv)
+    heads(v if cache is not None else None, "v", n_kv)
+    heads(q_out, "q_out", n_q)
+    heads(k_out, "k_out", n_kv)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _need(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
+        if positions is None:
+            _refuse("positions needed")
+        _need(positions, "positions", torch.int32, (T,), dev)
+    for t, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+        if t is not None:
+            _need(t, name, torch.float32, (D,), dev)
+    if cache is not None:
+        if cache.device != dev:
+            _refuse(f"the cache is on {cache.device}, q and k on {dev}")
+        if slots is None:
+            _refuse("slots needed with a cache")
+        _need(slots, "slots", torch.int64, (T,), dev)
+    if T == 0:
+        return
+    _call(lib().moe_qk_norm_rope, dev, stream, refs[0], refs[1], refs[2], _dtype_code(some), T, n_q, n_kv, D,
+          _ptr(positions), _ptr(inv_freq), rot, int(interleaved), rope_scale, _ptr(q_gain), _ptr(k_gain), eps, refs[3],
+          refs[4], None if cache is None else cache.ref, layer, None if cache is None else slots.data_ptr())
+
+
+def moe_rope_frequencies(rotary_dim: int, base: float = 10000.0, kind: int = MOE_ROPE_PLAIN, factor: float = 1.0,
+                         original_length: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                         device=None):
+    """(inv_freq, rope_scale): float64 [rotary_dim / 2] on `device` and the factor on the rotated values."""
+    import torch
+    out = torch.empty(max(0, rotary_dim // 2), dtype=torch.float64)
+    scale = _f()
+    _check(lib().moe_rope_frequencies(kind, rotary_dim, base, factor, original_length, beta_fast, beta_slow,
+                                      out.data_ptr(), ctypes.byref(scale)))
+    return (out if device is None else out.to(device)), scale.value
+
+
+def moe_attention_decode_workspace_bytes(n_q: int, n_kv: int, head_dim: int) -> int:
+    return int(lib().moe_attention_decode_workspace_bytes(n_q, n_kv, head_dim))
+
+
+def moe_attention_decode(q, cache: MoeKvCache, block_tables, seq_lens, out, scale: float, window: int = 0,
+                         layer: int = 0, lse=None, workspace=None, stream=None) -> None:
+    """Attention of one new token per sequence, q [B, n_q, D], over its seq_lens[b] cached keys (block_tables
+    int32 [B, max_pages]) into out [B, n_q, D] and, where given, lse float32 [B, n_q]. workspace: a
+    uint8 tensor of moe_attention_decode_workspace_bytes; None allocates it for this call (from the
+    stream's own memory pool, a captured graph's under capture)."""
+    import torch
+    if q.dim() != 3:
+        _refuse("q of shape [B, n_q, head_dim] needed")
+    shape = tuple(q.shape)
+    B, n_q, D = shape
+    dev = q.device
+    if D != cache.head_dim or cache.device != dev:
+        _refuse(f"q of {D} on {dev} over a cache of {cache.head_dim} on {cache.device}")
+    qh = _heads(q, "q", shape, q.dtype, dev)
+    oh = _heads(out, "out", shape, q.dtype, dev)
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or block_tables.dtype != torch.int32 or \
+            block_tables.device != dev or block_tables.stride(1) != 1:
+        _refuse(f"block_tables: need int32 [{B}, max_pages] with contiguous rows on {dev}")
+    _need(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, n_q), dev)
+    if B == 0:
+        return
+    cols = block_tables.shape[1]
+    if workspace is None:
+        need = lib().moe_attention_decode_workspace_bytes(n_q, cache.n_kv, D)
+        if stream is None or dev.type != "cuda":
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:   # from the pool of the stream that will use it
+            s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+            with torch.cuda.stream(s):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        _refuse(f"workspace: need a contiguous tensor on {dev}")
+    _call(lib().moe_attention_decode, dev, stream, ctypes.byref(qh), _dtype_code(q), cache.ref, layer,
+          block_tables.data_ptr(), block_tables.stride(0) if B > 1 else cols, cols, seq_lens.data_ptr(), B, n_q, scale,
+          window, ctypes.byref(oh), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def _host_pages(v, name):
+    """A host list of pages as a contiguous int32 CPU tensor."""
+    import torch
+    t = v if isinstance(v, torch.Tensor) else torch.as_tensor(v, dtype=torch.int32)
+    if t.device.type != "cpu" or t.dim() != 1 or t.dtype != torch.int32:
+        _refuse(f"{name}: a list or a one-dimensional int32 tensor on the host needed")
+    return t.contiguous()
+
+
+def moe_copy_pages(cache: MoeKvCache, src, dst, block_tables=None, stream=None) -> None:
+    """Page dst[i] = page src[i] of K and V in every layer of the cache (src, dst: host lists or int32 CPU
+    tensors). With block_tables (int32 [rows, cols] on the device) it is a move: entries equal to
+    src[i] become dst[i]."""
+    import torch
+    src, dst = _host_pages(src, "src"), _host_pages(dst, "dst")
+    if len(src) != len(dst):
+        _refuse(f"{len(src)} sources, {len(dst)} destinations")
+    if len(src) == 0:
+        return
+    rows = cols = stride = 0
+    if block_tables is not None:
+        if block_tables.dim() != 2 or block_tables.dtype != torch.int32 or block_tables.device != cache.device or \
+                block_tables.stride(1) != 1:
+            _refuse(f"block_tables: need int32 [rows, cols] with contiguous rows on {cache.device}")
+        rows, cols = block_tables.shape
+        stride = block_tables.stride(0) if rows > 1 else cols
+    _call(lib().moe_copy_pages, cache.device, stream, cache.ref, src.data_ptr(), dst.data_ptr(), len(src),
+          _ptr(block_tables), stride, rows, cols)
+
+
+def moe_cache_check(device=None, stream=None) -> None:
+    """Synchronise the stream and raise MoeError if a call since the last check met a page, length or slot out of range."""
+    import torch
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    _call(lib().moe_cache_check, dev, stream)

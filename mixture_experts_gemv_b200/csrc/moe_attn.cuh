@@ -1,0 +1,74 @@
+// moe_attn.cuh -- what the attention operators share: the cache as the kernels see it, the
+// launch parameters, and the host prototypes of their launchers.
+#pragma once
+
+#include "moe_common.cuh"
+
+// Device error codes of the cache operators (their error word belongs to moe_attn_api.cu).
+#define MOE_DEV_ERR_BAD_PAGE 3u     // a block-table entry inside a sequence is outside [0, num_pages)
+#define MOE_DEV_ERR_BAD_LENGTH 4u   // a sequence length is negative or longer than its block table
+#define MOE_DEV_ERR_BAD_SLOT 5u     // a slot is past the cache's last row
+
+// Grid limit of the one-token attention kernel: its workspace holds two pieces a CTA.
+constexpr int MOE_ATTN_MAX_CTAS = 640;
+// Tokens a CTA takes at a time (16 a warp), and head rows x padded head width it keeps.
+constexpr int MOE_ATTN_CHUNK = 64;
+constexpr int MOE_ATTN_ROWS_X_WIDTH = 4096;
+
+// Head width the kernel is compiled for that holds D, and the most head rows it takes at once.
+__host__ __device__ inline int moe_attn_width(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : (D <= 256 ? 256 : 512)); }
+// Query heads of one KV head that a CTA takes together (8 per MMA column tile): the fewest
+// column tiles that hold the group, up to the registers' limit of 512 / width tiles.
+__host__ __device__ inline int moe_attn_tiles(int D, int group) {
+  const int most = 512 / moe_attn_width(D);
+  int nt = 1;
+  while (nt < most && 8 * nt < group) nt *= 2;
+  return nt;
+}
+
+struct AttnParams {
+  const void *q;
+  long long q_tok, q_head;               // elements
+  const char *k, *v;
+  long long page_b, tok_b, head_b;       // bytes
+  const int32_t *tables;
+  long long table_stride;
+  int max_pages;
+  const int32_t *lens;
+  int B, nq, nkv, D, group, n_groups;    // group = nq / nkv; n_groups: CTA passes over a KV head's group
+  int page_size, num_pages, window;
+  float scale_log2;                      // scale * log2(e) * k_scale
+  float v_scale;
+  void *out;
+  long long out_tok, out_head;
+  float *lse;                            // [B, nq] or null
+  float *ws_o;                           // [2 CTAs][rows][D] unnormalised partial sums
+  float2 *ws_ml;                         // [2 CTAs][rows] running maximum (log2) and sum
+  int4 *rec;                             // [CTAs] the segment that starts in a CTA and ends in a later one
+  uint32_t *err;
+};
+
+struct RopeParams {
+  const void *q, *k, *v;
+  long long q_tok, q_head, k_tok, k_head, v_tok, v_head;   // elements
+  void *q_out, *k_out;
+  long long qo_tok, qo_head, ko_tok, ko_head;
+  const int32_t *positions;
+  const double *inv_freq;
+  const float *q_gain, *k_gain;
+  float eps, rope_scale;
+  int T, nq, nkv, D, rot;
+  char *ck, *cv;                           // cache, or null
+  long long page_b, tok_b, head_b;         // bytes
+  long long n_slots;
+  int page_size;
+  float k_scale, v_scale;
+  const int64_t *slots;
+  uint32_t *err;
+};
+
+// dtype / cache_dtype: MOE_DT_*. All return 0, or -1 after a CUDA error.
+int moe_launch_attn_bf16(const AttnParams &p, int num_sms, cudaStream_t s);   // bf16 q and cache
+int moe_launch_attn_f16(const AttnParams &p, int num_sms, cudaStream_t s);    // fp16 q and cache
+int moe_launch_attn_e4m3(const AttnParams &p, int num_sms, bool q_bf16, cudaStream_t s);   // e4m3 cache
+int moe_launch_rope(const RopeParams &p, int dtype, bool interleaved, bool cache_e4m3, int num_sms, cudaStream_t s);
