@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
@@ -62,16 +63,9 @@ _f = ctypes.c_float
 _d = ctypes.c_double
 
 
-class _KvCacheStruct(ctypes.Structure):
-    """moe_kv_cache"""
-    _fields_ = [("k", _p), ("v", _p), ("dtype", _i), ("n_layers", _i), ("num_pages", _i), ("page_size", _i),
-                ("n_kv", _i), ("head_dim", _i), ("layer_stride", _ll), ("page_stride", _ll), ("token_stride", _ll),
-                ("head_stride", _ll), ("k_scale", _f), ("v_scale", _f)]
-
-
-class _HeadsStruct(ctypes.Structure):
-    """moe_heads"""
-    _fields_ = [("p", _p), ("token_stride", _ll), ("head_stride", _ll)]
+# moe_kv_cache and moe_heads, packed as C lays them out
+_KV_CACHE = struct.Struct("@PPiiiiiiqqqqff")
+_HEADS = struct.Struct("@Pqq")
 
 
 def lib():
@@ -298,50 +292,68 @@ def moe_debug_inject(fault: int) -> None:
 #
 # These take torch tensors with their shapes and strides (the C entries take pointers and
 # strides), run on the tensors' device whichever device is current, and check here what the
-# library cannot see: types, devices and sizes.
+# library cannot see: types, devices and sizes. A call is a few microseconds of host time, so
+# the descriptors are packed into bytes rather than built as ctypes structures.
+
+_torch = None        # torch and the codes of its types, at the first call
+_dtype_codes = None
+_raw_stream = None
+
+
+def _setup():
+    global _torch, _dtype_codes, _raw_stream
+    import torch
+    _dtype_codes = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float8_e4m3fn: MOE_DT_E4M3}
+    # the current stream's handle without a Stream object around it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+
 
 def _refuse(msg: str):
     raise MoeError(MOE_ERR_BAD_ARG, msg)
 
 
-def _dtype_code(t) -> int:
-    import torch
-    code = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float8_e4m3fn: MOE_DT_E4M3}.get(t.dtype)
+def _dtype_code(dtype) -> int:
+    code = _dtype_codes.get(dtype)
     if code is None:
-        _refuse(f"{t.dtype} is neither bf16, fp16 nor e4m3")
+        _refuse(f"{dtype} is neither bf16, fp16 nor e4m3")
     return code
 
 
-def _need(t, name, dtype, shape, device, dense=True):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or (dense and not t.is_contiguous()):
-        _refuse(f"{name}: need a {'contiguous ' if dense else ''}{dtype} tensor of shape {tuple(shape)} on {device}, "
+def _need(t, name, dtype, shape, device):
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                 f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
 def _heads(t, name, shape, dtype, device):
     """moe_heads of a [T, heads, head_dim] tensor."""
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
-        _refuse(f"{name}: need {dtype} {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    st = t.stride()
-    if st[2] != 1:
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        _refuse(f"{name}: need {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    token, head, one = t.stride()
+    if one != 1:
         _refuse(f"{name}: the elements of a head must be contiguous")
-    return _HeadsStruct(t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
+    return _HEADS.pack(t.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0)
 
 
 def _call(fn, device, stream, *args):
     """fn(*args, stream) with the tensors' device current; stream None: its current stream."""
-    import torch
+    index = device.index
     if device.type != "cuda":
         _refuse(f"tensors must be on a CUDA device, not {device}")
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream))
+    if _torch._C._cuda_getDevice() == index:
+        rc = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, stream))
+        with _torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != MOE_OK:
+        _check(rc)
 
 
 class MoeKvCache:
@@ -351,23 +363,29 @@ class MoeKvCache:
     float8_e4m3fn (a stored value stands for value * scale)."""
 
     def __init__(self, k, v, layout: str = "NHD", k_scale: float = 1.0, v_scale: float = 1.0):
-        if layout not in ("NHD", "HND"):
-            _refuse(f"unknown layout {layout!r}")
+        if _torch is None:
+            _setup()
         shape, st = k.shape, k.stride()
-        if len(shape) == 4:
-            shape, st = (1,) + tuple(shape), (0,) + st
-        if len(shape) != 5 or v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype or v.device != k.device:
+        if v.shape != shape or v.stride() != st or v.dtype != k.dtype or v.device != k.device or len(shape) not in (4, 5):
             _refuse("k and v need the same shape, [(layers,) pages, ...], strides, type and device")
-        if st[4] != 1 and shape[4] > 1:
+        layers, layer_st = (1, 0) if len(shape) == 4 else (shape[0], st[0])
+        pages, a, b, dim = shape[-4:]
+        page_st, a_st, b_st, one = st[-4:]
+        if layout == "NHD":
+            tokens, heads, token_st, head_st = a, b, a_st, b_st
+        elif layout == "HND":
+            tokens, heads, token_st, head_st = b, a, b_st, a_st
+        else:
+            _refuse(f"unknown layout {layout!r}")
+        if one != 1 and dim > 1:
             _refuse("the elements of a head must be contiguous")
-        token, head = (2, 3) if layout == "NHD" else (3, 2)
         self.k, self.v, self.layout, self.device, self.dtype = k, v, layout, k.device, k.dtype
-        self.n_layers, self.num_pages, self.page_size = shape[0], shape[1], shape[token]
-        self.n_kv, self.head_dim = shape[head], shape[4]
-        st = [s if n > 1 else 0 for s, n in zip(st, shape)]
-        self.struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _dtype_code(k), shape[0], shape[1], shape[token],
-                                     shape[head], shape[4], st[0], st[1], st[token], st[head], k_scale, v_scale)
-        self.ref = ctypes.byref(self.struct)
+        self.n_layers, self.num_pages, self.page_size, self.n_kv, self.head_dim = layers, pages, tokens, heads, dim
+        self.k_scale, self.v_scale = k_scale, v_scale
+        # the stride of a dimension of one is not used and may be anything
+        self.packed = _KV_CACHE.pack(k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), layers, pages, tokens, heads, dim,
+                                     layer_st if layers > 1 else 0, page_st if pages > 1 else 0,
+                                     token_st if tokens > 1 else 0, head_st if heads > 1 else 0, k_scale, v_scale)
 
 
 def moe_qk_norm_rope(q, k, v, positions, inv_freq, q_gain=None, k_gain=None, eps: float = 1e-6,
@@ -376,48 +394,42 @@ def moe_qk_norm_rope(q, k, v, positions, inv_freq, q_gain=None, k_gain=None, eps
     """Norms of q [T, n_q, D] and k [T, n_kv, D] per head, rotation by positions (int32 [T]) and inv_freq
     (float64 [rotary_dim / 2], None: no rotation), into q_out and k_out and, with v, into `cache` at
     slots (int64 [T], negative: not stored). q or k may be None."""
-    import torch
-    some = q if q is not None else k
-    if some is None or some.dim() != 3:
+    if _torch is None:
+        _setup()
+    some = k if q is None else q
+    if some is None or some.dim() != 3 or (k is not None and k.dim() != 3):
         _refuse("q or k of shape [T, heads, head_dim] needed")
     T, _, D = some.shape
     dev, dt = some.device, some.dtype
-    refs = []
-
-    def heads(t, name, n):
-        if t is None:
-            refs.append(None)
-        else:
-            refs.append(ctypes.byref(_heads(t, name, (T, n, D), dt, dev)))
-
     n_q = 0 if q is None else q.shape[1]
-    n_kv = 0 if k is None or k.dim() != 3 else k.shape[1]
-    heads(q, "q", n_q)
-    heads(k, "k", n_kv)
-    heads(v if cache is not None else None, "v", n_kv)
-    heads(q_out, "q_out", n_q)
-    heads(k_out, "k_out", n_kv)
-    rot = 0
+    n_kv = 0 if k is None else k.shape[1]
+    of_q, of_k = (T, n_q, D), (T, n_kv, D)
+    ph = [None if t is None else _heads(t, name, shape, dt, dev)
+          for t, name, shape in ((q, "q", of_q), (k, "k", of_k), (None if cache is None else v, "v", of_k),
+                                 (q_out, "q_out", of_q), (k_out, "k_out", of_k))]
+    rot, p_pos, p_freq = 0, None, None
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _need(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
+        half = inv_freq.numel()
+        p_freq = _need(inv_freq, "inv_freq", _torch.float64, (half,), dev)
         if positions is None:
             _refuse("positions needed")
-        _need(positions, "positions", torch.int32, (T,), dev)
-    for t, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
-        if t is not None:
-            _need(t, name, torch.float32, (D,), dev)
+        p_pos = _need(positions, "positions", _torch.int32, (T,), dev)
+        rot = 2 * half
+    p_qg = None if q_gain is None else _need(q_gain, "q_gain", _torch.float32, (D,), dev)
+    p_kg = None if k_gain is None else _need(k_gain, "k_gain", _torch.float32, (D,), dev)
+    packed = p_slots = None
     if cache is not None:
         if cache.device != dev:
             _refuse(f"the cache is on {cache.device}, q and k on {dev}")
         if slots is None:
             _refuse("slots needed with a cache")
-        _need(slots, "slots", torch.int64, (T,), dev)
+        p_slots = _need(slots, "slots", _torch.int64, (T,), dev)
+        packed = cache.packed
+    code = _dtype_code(dt)
     if T == 0:
         return
-    _call(lib().moe_qk_norm_rope, dev, stream, refs[0], refs[1], refs[2], _dtype_code(some), T, n_q, n_kv, D,
-          _ptr(positions), _ptr(inv_freq), rot, int(interleaved), rope_scale, _ptr(q_gain), _ptr(k_gain), eps, refs[3],
-          refs[4], None if cache is None else cache.ref, layer, None if cache is None else slots.data_ptr())
+    _call(lib().moe_qk_norm_rope, dev, stream, ph[0], ph[1], ph[2], code, T, n_q, n_kv, D, p_pos, p_freq, rot,
+          1 if interleaved else 0, rope_scale, p_qg, p_kg, eps, ph[3], ph[4], packed, layer, p_slots)
 
 
 def moe_rope_frequencies(rotary_dim: int, base: float = 10000.0, kind: int = MOE_ROPE_PLAIN, factor: float = 1.0,
@@ -440,47 +452,48 @@ def moe_attention_decode(q, cache: MoeKvCache, block_tables, seq_lens, out, scal
                          layer: int = 0, lse=None, workspace=None, stream=None) -> None:
     """Attention of one new token per sequence, q [B, n_q, D], over its seq_lens[b] cached keys (block_tables
     int32 [B, max_pages]) into out [B, n_q, D] and, where given, lse float32 [B, n_q]. workspace: a
-    uint8 tensor of moe_attention_decode_workspace_bytes; None allocates it for this call (from the
-    stream's own memory pool, a captured graph's under capture)."""
-    import torch
+    tensor of at least moe_attention_decode_workspace_bytes bytes; None allocates it for this call (from
+    the stream's own memory pool, a captured graph's under capture)."""
     if q.dim() != 3:
         _refuse("q of shape [B, n_q, head_dim] needed")
-    shape = tuple(q.shape)
+    shape, dev, dt = q.shape, q.device, q.dtype
     B, n_q, D = shape
-    dev = q.device
     if D != cache.head_dim or cache.device != dev:
         _refuse(f"q of {D} on {dev} over a cache of {cache.head_dim} on {cache.device}")
-    qh = _heads(q, "q", shape, q.dtype, dev)
-    oh = _heads(out, "out", shape, q.dtype, dev)
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or block_tables.dtype != torch.int32 or \
-            block_tables.device != dev or block_tables.stride(1) != 1:
-        _refuse(f"block_tables: need int32 [{B}, max_pages] with contiguous rows on {dev}")
-    _need(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, (B, n_q), dev)
+    ph_q = _heads(q, "q", shape, dt, dev)
+    ph_out = _heads(out, "out", shape, dt, dev)
+    if block_tables.dim() != 2 or block_tables.dtype != _torch.int32 or block_tables.device != dev:
+        _refuse(f"block_tables: need int32 [{B}, max_pages] on {dev}")
+    rows, cols = block_tables.shape
+    table_st, one = block_tables.stride()
+    if rows != B or (one != 1 and cols > 1):
+        _refuse(f"block_tables: need int32 [{B}, max_pages] with contiguous rows")
+    p_lens = _need(seq_lens, "seq_lens", _torch.int32, (B,), dev)
+    p_lse = None if lse is None else _need(lse, "lse", _torch.float32, (B, n_q), dev)
+    code = _dtype_code(dt)
     if B == 0:
         return
-    cols = block_tables.shape[1]
+    L = lib()
     if workspace is None:
-        need = lib().moe_attention_decode_workspace_bytes(n_q, cache.n_kv, D)
+        size = L.moe_attention_decode_workspace_bytes(n_q, cache.n_kv, D)
         if stream is None or dev.type != "cuda":
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = _torch.empty(size, dtype=_torch.uint8, device=dev)
         else:   # from the pool of the stream that will use it
-            s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
-            with torch.cuda.stream(s):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        _refuse(f"workspace: need a contiguous tensor on {dev}")
-    _call(lib().moe_attention_decode, dev, stream, ctypes.byref(qh), _dtype_code(q), cache.ref, layer,
-          block_tables.data_ptr(), block_tables.stride(0) if B > 1 else cols, cols, seq_lens.data_ptr(), B, n_q, scale,
-          window, ctypes.byref(oh), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            s = _torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+            with _torch.cuda.stream(s):
+                workspace = _torch.empty(size, dtype=_torch.uint8, device=dev)
+    else:
+        if workspace.device != dev or not workspace.is_contiguous():
+            _refuse(f"workspace: need a contiguous tensor on {dev}")
+        size = workspace.numel() * workspace.element_size()
+    _call(L.moe_attention_decode, dev, stream, ph_q, code, cache.packed, layer, block_tables.data_ptr(),
+          table_st if B > 1 else cols, cols, p_lens, B, n_q, scale, window, ph_out, p_lse, workspace.data_ptr(), size)
 
 
 def _host_pages(v, name):
     """A host list of pages as a contiguous int32 CPU tensor."""
-    import torch
-    t = v if isinstance(v, torch.Tensor) else torch.as_tensor(v, dtype=torch.int32)
-    if t.device.type != "cpu" or t.dim() != 1 or t.dtype != torch.int32:
+    t = v if isinstance(v, _torch.Tensor) else _torch.as_tensor(v, dtype=_torch.int32)
+    if t.device.type != "cpu" or t.dim() != 1 or t.dtype != _torch.int32:
         _refuse(f"{name}: a list or a one-dimensional int32 tensor on the host needed")
     return t.contiguous()
 
@@ -489,25 +502,33 @@ def moe_copy_pages(cache: MoeKvCache, src, dst, block_tables=None, stream=None) 
     """Page dst[i] = page src[i] of K and V in every layer of the cache (src, dst: host lists or int32 CPU
     tensors). With block_tables (int32 [rows, cols] on the device) it is a move: entries equal to
     src[i] become dst[i]."""
-    import torch
     src, dst = _host_pages(src, "src"), _host_pages(dst, "dst")
-    if len(src) != len(dst):
-        _refuse(f"{len(src)} sources, {len(dst)} destinations")
-    if len(src) == 0:
-        return
-    rows = cols = stride = 0
+    n = len(src)
+    if n != len(dst):
+        _refuse(f"{n} sources, {len(dst)} destinations")
+    rows = cols = table_st = 0
+    p_tables = None
     if block_tables is not None:
-        if block_tables.dim() != 2 or block_tables.dtype != torch.int32 or block_tables.device != cache.device or \
-                block_tables.stride(1) != 1:
-            _refuse(f"block_tables: need int32 [rows, cols] with contiguous rows on {cache.device}")
+        if block_tables.dim() != 2 or block_tables.dtype != _torch.int32 or block_tables.device != cache.device:
+            _refuse(f"block_tables: need int32 [rows, cols] on {cache.device}")
         rows, cols = block_tables.shape
-        stride = block_tables.stride(0) if rows > 1 else cols
-    _call(lib().moe_copy_pages, cache.device, stream, cache.ref, src.data_ptr(), dst.data_ptr(), len(src),
-          _ptr(block_tables), stride, rows, cols)
+        table_st, one = block_tables.stride()
+        if one != 1 and cols > 1:
+            _refuse("block_tables: rows must be contiguous")
+        if rows <= 1:
+            table_st = cols
+        p_tables = block_tables.data_ptr()
+    if n == 0:
+        return
+    _call(lib().moe_copy_pages, cache.device, stream, cache.packed, src.data_ptr(), dst.data_ptr(), n, p_tables,
+          table_st, rows, cols)
 
 
 def moe_cache_check(device=None, stream=None) -> None:
     """Synchronise the stream and raise MoeError if a call since the last check met a page, length or slot out of range."""
-    import torch
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if _torch is None:
+        _setup()
+    dev = _torch.device("cuda" if device is None else device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = _torch.device("cuda", _torch.cuda.current_device())
     _call(lib().moe_cache_check, dev, stream)

@@ -9,11 +9,8 @@
 #define MOE_DEV_ERR_BAD_LENGTH 4u   // a sequence length is negative or longer than its block table
 #define MOE_DEV_ERR_BAD_SLOT 5u     // a slot is past the cache's last row
 
-// Grid limit of the one-token attention kernel: its workspace holds two pieces a CTA.
-constexpr int MOE_ATTN_MAX_CTAS = 640;
-// Tokens a CTA takes at a time (16 a warp), and head rows x padded head width it keeps.
-constexpr int MOE_ATTN_CHUNK = 64;
-constexpr int MOE_ATTN_ROWS_X_WIDTH = 4096;
+// Most warps of the one-token attention kernel: its workspace holds two pieces for each.
+constexpr int MOE_ATTN_MAX_WORKERS = 1280;
 
 // Head width the kernel is compiled for that holds D, and the most head rows it takes at once.
 __host__ __device__ inline int moe_attn_width(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : (D <= 256 ? 256 : 512)); }
@@ -33,18 +30,20 @@ struct AttnParams {
   long long page_b, tok_b, head_b;       // bytes
   const int32_t *tables;
   long long table_stride;
-  int max_pages;
+  int max_tokens;                        // that a block table can hold
   const int32_t *lens;
   int B, nq, nkv, D, group, n_groups;    // group = nq / nkv; n_groups: CTA passes over a KV head's group
   int page_size, num_pages, window;
+  int groups_of_8;                       // 8 tokens from a multiple of 8 on always lie in one page
   float scale_log2;                      // scale * log2(e) * k_scale
   float v_scale;
   void *out;
   long long out_tok, out_head;
   float *lse;                            // [B, nq] or null
-  float *ws_o;                           // [2 CTAs][rows][D] unnormalised partial sums
-  float2 *ws_ml;                         // [2 CTAs][rows] running maximum (log2) and sum
-  int4 *rec;                             // [CTAs] the segment that starts in a CTA and ends in a later one
+  float *ws_o;                           // [2 workers][D / 16][column tiles][32 lanes][4] unnormalised sums
+  float2 *ws_ml;                         // [2 workers][rows] maximum (log2) and sum
+  int4 *rec;                             // (first worker + 1 or 0, sequence, segment, last worker) of cut segments
+  int rec_by_segment;                    // one record a segment, else one a worker
   uint32_t *err;
 };
 

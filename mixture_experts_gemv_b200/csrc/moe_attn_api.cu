@@ -285,15 +285,15 @@ int moe_rope_frequencies(int kind, int rotary_dim, double base, double factor, d
   return MOE_OK;
 }
 
-// Layout of the workspace: partial sums, then (maximum, sum) pairs, then the CTAs' records.
+// Layout of the workspace: partial sums, then (maximum, sum) pairs, then the records of cut segments.
 static size_t attn_rows(int n_q, int n_kv, int D) { return 8 * (size_t)moe_attn_tiles(D, n_q / n_kv); }
-static size_t attn_o_bytes(size_t rows, int D) { return 2ull * MOE_ATTN_MAX_CTAS * rows * D * 4; }
-static size_t attn_ml_bytes(size_t rows) { return 2ull * MOE_ATTN_MAX_CTAS * rows * 8; }
+static size_t attn_o_bytes(size_t rows, int D) { return 2ull * MOE_ATTN_MAX_WORKERS * rows * D * 4; }
+static size_t attn_ml_bytes(size_t rows) { return 2ull * MOE_ATTN_MAX_WORKERS * rows * 8; }
 
 size_t moe_attention_decode_workspace_bytes(int n_q, int n_kv, int head_dim) {
   if (n_q < 1 || n_kv < 1 || n_q % n_kv || head_dim < 16 || head_dim > 512 || head_dim % 16) return 0;
   const size_t rows = attn_rows(n_q, n_kv, head_dim);
-  return attn_o_bytes(rows, head_dim) + attn_ml_bytes(rows) + MOE_ATTN_MAX_CTAS * sizeof(int4);
+  return attn_o_bytes(rows, head_dim) + attn_ml_bytes(rows) + MOE_ATTN_MAX_WORKERS * sizeof(int4);
 }
 
 int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cache, int layer, const int32_t *block_tables,
@@ -338,7 +338,7 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
   p.head_b = cache->head_stride * es;
   p.tables = block_tables;
   p.table_stride = table_stride;
-  p.max_pages = max_pages;
+  p.max_tokens = max_pages * cache->page_size;
   p.lens = seq_lens;
   p.B = B;
   p.nq = n_q;
@@ -349,6 +349,7 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
   p.page_size = cache->page_size;
   p.num_pages = cache->num_pages;
   p.window = window;
+  p.groups_of_8 = cache->page_size % 8 == 0 && p.tok_b < (1ll << 28);   // row offsets within a group in 32 bits
   p.scale_log2 = (float)((double)scale * cache->k_scale * 1.4426950408889634);
   p.v_scale = cache->v_scale;
   p.out = out->p, p.out_tok = out->token_stride, p.out_head = out->head_stride;

@@ -13,16 +13,15 @@
 // memory once, and O takes D / 4 registers a thread for 8 heads. (With heads as rows, half the
 // tile would be empty and O would not fit at D = 512.)
 //
-// Each warp takes 16 tokens at a time through its own ring of cp.async copies (K rows, then V
-// rows), so the loop has no block barrier. A block takes 64 tokens at a time (16 per warp) and
-// joins its four warps' (maximum, sum, O) through shared memory at the end of a segment = the
-// tokens of one (sequence, KV head, head group).
-//
-// Work split: the 64-token chunks of all segments are numbered through and cut into equal
-// ranges, one per CTA of a grid that fills the GPU once, whatever the lengths are. A segment
-// cut by a range's end leaves unnormalised pieces in the workspace (at most two per CTA); the
-// join kernel, launched behind with programmatic dependent launch, sums them in CTA order. No
-// atomics: outputs repeat bit for bit.
+// Warps are independent workers without a block barrier in their loop. A unit of work is 16 or 32
+// tokens (one or two row tiles) of one (sequence, KV head, head group) = segment. The units of all
+// segments are numbered through and cut into equal ranges, one per warp of a grid that fills the
+// GPU once, whatever the lengths are. A warp streams its units' K and V rows through a ring of
+// cp.async copies of its own, which runs ahead over the ends of segments. A segment that a range
+// holds whole is written out by its warp; one cut by a range's end leaves unnormalised pieces in
+// the workspace (at most two per warp, in fragment order; a block in the middle of a long segment
+// joins its warps' first), and the join kernel, launched behind with programmatic dependent
+// launch, sums them in order. No atomics: outputs repeat bit for bit.
 //
 // Precision: K Q^T products are exact, summed in FP32; the softmax runs in FP32 (base 2); P is
 // rounded to the 16-bit type of the V product (half a step, 2^-9 or 2^-12 of each p, the sum l
@@ -87,6 +86,11 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {   // the low t
 __device__ __forceinline__ void copy16(uint32_t dst, const char *src, bool ok) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
+// The same where `on` is not 0, without a branch; nothing is written otherwise.
+__device__ __forceinline__ void copy16_if(uint32_t dst, const char *src, int on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t"
+               "@p cp.async.cg.shared.global.L2::128B [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src), "r"(on) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -97,250 +101,441 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // Compile-time shape: W padded head width, NT column tiles of 8 heads, ES bytes an element.
 template <int W, int NT, int ES> struct Shape {
-  static constexpr int kRow = W * ES;             // bytes of a staged row
-  static constexpr int kUnit = 16 * kRow;         // 16 tokens of K or of V
-  // Units in a warp's ring. 96 KB a CTA (two CTAs an SM) up to W = 128, 192 KB above.
-  static constexpr int kUnits = kUnit <= 2048 ? 12 : (kUnit <= 8192 ? 6 : 3);
+  static constexpr int kRow = W * ES;               // bytes of a staged row
+  // 16-token row tiles a warp takes per step: two where a row is short, which halves the share
+  // of the softmax's shuffles and of the loop (not with 32 heads and more: registers)
+  static constexpr int kTiles = kRow <= 256 && NT <= 2 ? 2 : 1;
+  static constexpr int kTok = 16 * kTiles;          // tokens of a unit
+  static constexpr int kUnit = kTok * kRow;         // bytes of its K or V rows
+  // Slots of kUnit in a warp's ring: 96 KB a CTA, two CTAs an SM (192 KB and one where a slot is
+  // 16 KB): at least 128 KB of copies in flight on an SM
+  static constexpr int kSlots = kUnit >= 16384 ? 3 : 24576 / kUnit;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kPitch = W + 4;            // floats; conflict-free C-fragment stores
-  static constexpr int kJoin = kWarps * kRows * kPitch * 4;
-  static constexpr int kRing = kWarps * kUnits * kUnit;
-  static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-  static constexpr int kChunks = kRow / 16;       // 16-byte pieces of a row
+  static constexpr int kSmem = kWarps * kSlots * kUnit;
+  static constexpr int kPieces = kRow / 16;         // 16-byte pieces of a row
   // XOR on a row's 16-byte pieces that spreads 8 consecutive rows over the banks
-  static __device__ __forceinline__ int swz(int r) { return kChunks >= 8 ? (r & 7) : ((r >> 1) & 3); }
+  static __device__ __forceinline__ constexpr int swz(int r) { return kPieces >= 8 ? (r & 7) : ((r >> 1) & 3); }
+  // Address of the k-th pair of pieces of the row whose first pair lies at base: the XOR touches
+  // the low three bits of a piece's number, the rest is an offset
+  static __device__ __forceinline__ constexpr uint32_t at(uint32_t base, int k) { return (base ^ (uint32_t)((k & 3) << 5)) + (k >> 2) * 128; }
 };
 
-// Chunks of a sequence and its first key. A bad length is cut to what the table can hold.
+// Keys [lo, len) of a sequence: n units from unit number lo / TOK on. A bad length is cut to what
+// the table can hold.
 struct Span {
-  int len, lo, first, n;
+  int len, lo, n;
 };
-__device__ __forceinline__ Span span_of(const AttnParams &p, int b) {
+template <int TOK> __device__ __forceinline__ Span span_of(const AttnParams &p, int b) {
   Span s;
   int len = p.lens[b];
-  const long long cap = (long long)p.max_pages * p.page_size;
-  if (len < 0 || len > cap) {
-    report_error(p.err, MOE_DEV_ERR_BAD_LENGTH, 0);
-    len = len < 0 ? 0 : (int)cap;
+  if ((unsigned)len > (unsigned)p.max_tokens) {
+    atomicCAS(p.err, 0u, MOE_DEV_ERR_BAD_LENGTH);
+    len = len < 0 ? 0 : p.max_tokens;
   }
   s.len = len;
   s.lo = p.window > 0 && len > p.window ? len - p.window : 0;
-  s.first = s.lo / MOE_ATTN_CHUNK;
-  s.n = len > 0 ? (len - 1) / MOE_ATTN_CHUNK + 1 - s.first : 0;
+  s.n = len > 0 ? (len - 1) / TOK + 1 - s.lo / TOK : 0;
   return s;
 }
 
-__device__ __forceinline__ long long shfl_up64(long long v, int d) { return __shfl_up_sync(0xffffffffu, v, d); }
+static __device__ __noinline__ long long quotient64(long long a, int b) { return a / b; }
+__device__ __forceinline__ long long quotient(long long a, int b) {   // a >= 0; 32-bit division where it fits
+  return (a >> 32) ? quotient64(a, b) : (long long)((unsigned)a / (unsigned)b);
+}
+
+// Equal ranges of `total` costs for at most `most` workers, each at least one: the first
+// `longer` workers have one more than `each`.
+struct Split {
+  int workers, longer;
+  long long each;
+  __device__ __forceinline__ Split(long long total, int most) {
+    workers = total < most ? (int)total : most;
+    each = workers ? quotient(total, workers) : 0;
+    longer = (int)(total - each * workers);
+  }
+  __device__ __forceinline__ long long first(int worker) const { return worker * each + min(worker, longer); }
+  __device__ __forceinline__ int owner(long long cost) const {
+    const long long head = longer * (each + 1);
+    return cost < head ? (int)quotient(cost, (int)each + 1) : longer + (int)quotient(cost - head, (int)each);
+  }
+};
+
+// Pieces of a segment cut over the workers [w0, w1]: a block whose four workers all lie strictly
+// inside (they then have nothing else) leaves one piece, as its first worker's.
+struct Block {
+  int at;
+  __device__ __forceinline__ explicit Block(int b) : at(b * kWarps) {}
+  __device__ __forceinline__ bool inside(int w0, int w1) const { return at > w0 && at + kWarps - 1 < w1; }
+};
+struct Pieces {
+  int w0, head, blocks, tail, count;   // workers before the whole blocks, blocks, first worker behind them
+  __device__ __forceinline__ Pieces(int first, int last, bool joined) {
+    w0 = first;
+    const int a = first / kWarps + 1, b = last / kWarps - 1;   // first and last whole block
+    blocks = joined && b >= a ? b - a + 1 : 0;
+    head = blocks ? a * kWarps - first : last - first + 1;
+    tail = (b + 1) * kWarps;
+    count = blocks ? head + blocks + last - tail + 1 : head;
+  }
+  __device__ __forceinline__ int worker(int i) const {
+    return i < head ? w0 + i : i < head + blocks ? (w0 / kWarps + 1 + i - head) * kWarps : tail + i - head - blocks;
+  }
+};
+
+// Two heads' maxima and sums (m, l, m, l) and a fragment of their unnormalised rows, joined from pieces.
+struct Joined {
+  float4 ml, acc;
+  __device__ __forceinline__ Joined() {
+    const float ninf = __int_as_float(0xff800000);
+    ml = make_float4(ninf, 0.f, ninf, 0.f);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void take(const float4 &pm, const float4 &v) {
+    const float ninf = __int_as_float(0xff800000);
+    const float m0 = fmaxf(ml.x, pm.x), m1 = fmaxf(ml.z, pm.z), b0 = m0 == ninf ? 0.f : m0, b1 = m1 == ninf ? 0.f : m1;
+    const float a0 = exp2_fast(ml.x - b0), a1 = exp2_fast(ml.z - b1), f0 = exp2_fast(pm.x - b0), f1 = exp2_fast(pm.z - b1);
+    ml = make_float4(m0, fmaf(ml.y, a0, f0 * pm.y), m1, fmaf(ml.w, a1, f1 * pm.w));
+    acc.x = fmaf(acc.x, a0, f0 * v.x);
+    acc.y = fmaf(acc.y, a1, f1 * v.y);
+    acc.z = fmaf(acc.z, a0, f0 * v.z);
+    acc.w = fmaf(acc.w, a1, f1 * v.w);
+  }
+};
+
+// A place in the numbering of units: unit i of n of segment seg of sequence b.
+template <int TOK> struct Cursor {
+  int b, seg, i;
+  Span sp;
+  __device__ __forceinline__ void next(const AttnParams &p, int segs) {   // not past the last unit
+    if (++i < sp.n) return;
+    i = 0;
+    if (++seg < segs) return;
+    seg = 0;
+#pragma unroll 1
+    do sp = span_of<TOK>(p, ++b);
+    while (sp.n == 0);
+  }
+  __device__ __forceinline__ int token() const { return (sp.lo / TOK + i) * TOK; }   // the unit's first
+};
+
+// One accumulator fragment (two heads' values at two elements, x inv) into the rows of a KV head's
+// group: out points at head 8 n, `heads` of them exist. 16 ES-dependent elements from 16 k on.
+template <typename TO, int ES>
+__device__ __forceinline__ void store_fragment(TO *out, long long out_head, int k, int heads, int lane, const float4 &v, float inv0, float inv1) {
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t lo = transposed8x8(Mma<TO>::pack(v.x * inv0, v.y * inv1)), hi = transposed8x8(Mma<TO>::pack(v.z * inv0, v.w * inv1));
+  if (g >= heads) return;
+  TO *row = out + g * out_head + 16 * k;
+  if constexpr (ES == 2) {   // rows g and g + 8 of the tile are elements g and g + 8
+    *reinterpret_cast<uint32_t *>(row + 2 * c) = lo;
+    *reinterpret_cast<uint32_t *>(row + 8 + 2 * c) = hi;
+  } else {                   // elements 2 g and 2 g + 1
+    *reinterpret_cast<uint2 *>(row + 4 * c) = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+  }
+}
 
 // T: type of the products. QB: q is bf16 (only read with ES == 1; else q has type T).
 template <typename T, int W, int NT, int ES, bool QB>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const AttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_constant__ AttnParams p) {
   using S = Shape<W, NT, ES>;
   using M = Mma<T>;
-  extern __shared__ __align__(128) char smem[];
-  __shared__ long long sh_scan[kWarps];
-  __shared__ long long sh_found[2];
-  __shared__ float sh_m[kWarps][S::kRows], sh_l[kWarps][S::kRows];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  using TO = std::conditional_t<ES == 1 && QB, __nv_bfloat16, T>;
+  constexpr unsigned kAll = 0xffffffffu;
+  extern __shared__ __align__(1024) char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
+  const float ninf = __int_as_float(0xff800000);
+  const uint32_t ring = smem_u32(smem) + warp * (S::kSlots * S::kUnit);
+  if (p.D < W) {   // the pieces past head_dim are never copied: zeros
+#pragma unroll 1
+    for (int i = lane * 16; i < S::kSlots * S::kUnit; i += 512)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(ring + i), "r"(0) : "memory");
+    __syncwarp();
+  }
+  pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the CTA's range of chunks
-  const int hs = p.nkv * p.n_groups;
-  long long total = 0;
-  for (int b = tid; b < p.B; b += kWarps * 32) total += span_of(p, b).n;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) sh_scan[warp] = total;
-  if (tid == 0) sh_found[0] = -1;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sh_scan[w];
-  __syncthreads();
-  total *= hs;
-  const long long ctas = total < (long long)gridDim.x ? total : (long long)gridDim.x;
-  const long long cta = blockIdx.x;
-  long long u = 0, u_end = 0;
-  if (cta < ctas) {
-    u = cta * total / ctas;
-    u_end = (cta + 1) * total / ctas;
+  // ---- the warp's range of units
+  const int segs = p.nkv * p.n_groups;
+  const int all_workers = kWarps * gridDim.x;
+  const int n_first = lane < p.B ? span_of<S::kTok>(p, lane).n : 0;   // of the first 32 sequences
+  long long units = n_first;
+  int filled = n_first > 0;   // sequences with a key
+#pragma unroll 1
+  for (int b = 32 + lane; b < p.B; b += 32) {
+    const int n = span_of<S::kTok>(p, b).n;
+    units += n;
+    filled += n > 0;
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    units += __shfl_xor_sync(kAll, units, o);
+    filled += __shfl_xor_sync(kAll, filled, o);
+  }
+  // A segment costs its units and, where workers have several, one more: its q, its ends and its
+  // result (eight one-unit segments in one warp's range took 5 to 8 us beside a 36 us stream of
+  // 40,000 tokens). Every worker's range still holds a unit: no two of these are neighbours.
+  const int extra = (units + filled) * segs >= 2ll * all_workers ? 1 : 0;
+  const Split split((units + extra * filled) * segs, all_workers);
+  const int workers = split.workers;
+  // Neighbours in the numbering are on different SMs where there is little to do, else in one
+  // block, which can then join its warps' pieces
+  const int worker = extra ? blockIdx.x * kWarps + warp : warp * gridDim.x + blockIdx.x;
   // sequences without a key: rows of zeros, lse = -inf
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (span_of(p, b).n) continue;
-    for (int i = tid; i < p.nq * p.D; i += kWarps * 32) {
-      const int h = i / p.D, d = i - h * p.D;
-      const long long at = (long long)b * p.out_tok + (long long)h * p.out_head + d;
-      if constexpr (ES == 1 && QB) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(0.f);
-      else static_cast<T *>(p.out)[at] = T(0.f);
-      if (p.lse && d == 0) p.lse[(long long)b * p.nq + h] = __int_as_float(0xff800000);
+#pragma unroll 1
+  for (int b = worker; b < p.B; b += all_workers) {
+    if (span_of<S::kTok>(p, b).n) continue;
+    if (p.rec_by_segment)
+#pragma unroll 1
+      for (int i = lane; i < segs; i += 32) p.rec[b * segs + i] = make_int4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int h = 0; h < p.nq; ++h) {
+#pragma unroll 1
+      for (int d = lane; d < p.D; d += 32) static_cast<TO *>(p.out)[(long long)b * p.out_tok + (long long)h * p.out_head + d] = TO(0.f);
+      if (p.lse && lane == 0) p.lse[(long long)b * p.nq + h] = ninf;
     }
   }
-  if (u >= u_end) {
-    if (tid == 0) p.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (worker >= workers) {
+    if (!p.rec_by_segment && lane == 0) p.rec[worker] = make_int4(0, 0, 0, 0);
     return;
   }
-  // ---- the sequence that holds chunk u
-  long long before = 0;   // chunks of the earlier sequences (for one head)
-  for (int base = 0; base < p.B; base += kWarps * 32) {
-    const int b = base + tid;
-    const long long n = b < p.B ? span_of(p, b).n : 0;
-    long long inc = n;
+  // Numbering of costs: a segment's extra one, then its units. The units at costs [from, to):
+  const long long from = split.first(worker), to = split.first(worker + 1);
+  Cursor<S::kTok> at;        // the unit that is computed next
+  long long seg_first = 0;   // cost number of its segment's start
+  int count = 0;             // the warp's units
+  {
+    long long before = 0, units_before = 0;   // costs and units of the earlier sequences
+    long long begin = -1;                     // units before `from`
+#pragma unroll 1
+    for (int base = 0;; base += 32) {
+      const int b = base + lane;
+      const long long n = base ? (b < p.B ? span_of<S::kTok>(p, b).n : 0) : n_first;
+      long long inc = n ? (n + extra) * segs : 0, inc_units = n * segs;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = shfl_up64(inc, o);
-      if (lane >= o) inc += t;
-    }
-    if (lane == 31) sh_scan[warp] = inc;
-    __syncthreads();
-    long long add = before, strip = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) add += sh_scan[w];
-      strip += sh_scan[w];
-    }
-    const long long lo = (add + inc - n) * hs, hi = (add + inc) * hs;
-    if (u >= lo && u < hi) {
-      sh_found[0] = b;
-      sh_found[1] = add + inc - n;
-    }
-    before += strip;
-    __syncthreads();
-    if (sh_found[0] >= 0) break;
-  }
-  int b = (int)sh_found[0];
-  long long seq_first = sh_found[1];
-  Span sp = span_of(p, b);
-
-  const uint32_t ring = smem_u32(smem) + warp * (S::kUnits * S::kUnit);
-  int4 rec = make_int4(0, 0, 0, 0);
-
-  while (u < u_end) {
-    const long long rel = u - seq_first * hs;
-    const int seg = (int)(rel / sp.n), i0 = (int)(rel - (long long)seg * sp.n);
-    const int cnt = (int)(u_end - u < (long long)(sp.n - i0) ? u_end - u : (long long)(sp.n - i0));
-    const int kvh = seg / p.n_groups, h0 = kvh * p.group + (seg - kvh * p.n_groups) * S::kRows;
-    const int heads = min(S::kRows, (kvh + 1) * p.group - h0);
-
-    // ---- loader state: this lane looks up row (lane & 15) of each 16-token unit
-    const int row = lane & 15;
-    const int t_first = (sp.first + i0) * MOE_ATTN_CHUNK + warp * 16;   // of the warp's first unit
-    const int32_t *table = p.tables + (long long)b * p.table_stride;
-    const char *kb = p.k + (long long)kvh * p.head_b, *vb = p.v + (long long)kvh * p.head_b;
-    int page = 0;
-    auto look_up = [&](int i) {   // block-table entry of this lane's row of the warp's i-th unit
-      const int t = t_first + i * MOE_ATTN_CHUNK + row;
-      page = 0;
-      if (i < cnt && t >= sp.lo && t < sp.len) page = __ldg(table + t / p.page_size);
-    };
-    long long off = 0;
-    bool ok = false;
-    auto locate = [&](int i) {
-      const int t = t_first + i * MOE_ATTN_CHUNK + row;
-      ok = i < cnt && t >= sp.lo && t < sp.len;
-      if (ok && (page < 0 || page >= p.num_pages)) {
-        report_error(p.err, MOE_DEV_ERR_BAD_PAGE, 0);
-        ok = false;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(kAll, inc, o), tu = __shfl_up_sync(kAll, inc_units, o);
+        if (lane >= o) inc += t, inc_units += tu;
       }
-      off = ok ? (long long)page * p.page_b + (long long)(t % p.page_size) * p.tok_b : 0;
-    };
-    auto issue = [&](const char *base, int slot) {
-      const uint32_t dst = ring + slot * S::kUnit;
-#pragma unroll
-      for (int j = 0; j < S::kUnit / 512; ++j) {
-        const int idx = j * 32 + lane, r = idx / S::kChunks, ch = idx % S::kChunks;
-        const long long ro = __shfl_sync(0xffffffffu, off, r);
-        const bool rok = __shfl_sync(0xffffffffu, (int)ok, r) && ch * (16 / ES) < p.D;
-        copy16(dst + r * S::kRow + ((ch ^ S::swz(r)) << 4), rok ? base + ro + ch * 16 : base, rok);
-      }
-      copy_commit();
-    };
-    const int units = 2 * cnt;   // K, V, K, V, ...
-    int next = 0, slot_in = 0;   // next unit to issue
-    auto issue_next = [&]() {
-      if (next < units) {
-        if (!(next & 1)) {
-          locate(next >> 1);
-          look_up((next >> 1) + 1);
-          issue(kb, slot_in);
+#pragma unroll 1
+      for (int end = 0; end < 2; ++end) {   // first `from`, then `to`: a cost's sequence, segment and unit
+        if ((end == 0) != (begin < 0)) continue;
+        const unsigned hit = __ballot_sync(kAll, end == 0 ? from < before + inc : to <= before + inc);
+        if (!hit) break;
+        const int src = __ffs(hit) - 1, sn = (int)__shfl_sync(kAll, n, src);
+        const long long first = before + __shfl_sync(kAll, inc, src) - (long long)(sn + extra) * segs;
+        const long long rel = (end == 0 ? from : to) - first;
+        const int seg = (int)quotient(rel, sn + extra);
+        const int i = max((int)(rel - (long long)seg * (sn + extra)) - extra, 0);
+        const long long mine = units_before + __shfl_sync(kAll, inc_units, src) - (long long)sn * segs + (long long)seg * sn + i;
+        if (end == 0) {
+          at.b = base + src;
+          at.seg = seg;
+          at.i = i;
+          seg_first = first + (long long)seg * (sn + extra);
+          begin = mine;
         } else {
-          issue(vb, slot_in);
+          count = (int)(mine - begin);
+        }
+      }
+      if (count) break;
+      before += __shfl_sync(kAll, inc, 31);
+      units_before += __shfl_sync(kAll, inc_units, 31);
+    }
+    at.sp = span_of<S::kTok>(p, at.b);
+  }
+
+  // ---- loader: runs ahead of the computation by the ring's slots, and its look-ups in the block
+  // tables by two units more
+  Cursor<S::kTok> ahead = at;   // the unit that is looked up next
+  int to_look_up = count, to_copy = count;
+  struct Found {                // a looked-up unit, as lane r holds it for token r
+    int page, in_page, kvh, first, last;   // tokens [first, last) of the unit are keys
+  } now{}, then{};
+  auto look_up = [&](Found &f) {
+    if (to_look_up <= 0) return;
+    const int t0 = ahead.token(), t = t0 + (lane & (S::kTok - 1));
+    f.first = max(ahead.sp.lo - t0, 0);
+    f.last = min(ahead.sp.len - t0, S::kTok);
+    f.kvh = ahead.seg / p.n_groups;
+    f.page = 0;
+    // with pages of whole 8-token groups, every lane of a group that holds a key has the group's page
+    const int lo = p.groups_of_8 ? ahead.sp.lo & ~7 : ahead.sp.lo, hi = p.groups_of_8 ? (ahead.sp.len + 7) & ~7 : ahead.sp.len;
+    if (t >= lo && t < hi) {
+      const unsigned e = (unsigned)t / (unsigned)p.page_size;
+      f.in_page = t - (int)e * p.page_size;
+      f.page = __ldg(p.tables + (long long)ahead.b * p.table_stride + e);
+    } else {
+      f.page = f.in_page = 0;
+    }
+    if (--to_look_up > 0) {
+      ahead.next(p, segs);
+      if (ahead.i == 0) {   // a new segment: its q rows on their way to L1 (a lane per 128 bytes)
+        const int kvh = ahead.seg / p.n_groups, h0 = kvh * p.group + (ahead.seg - kvh * p.n_groups) * S::kRows;
+        const int lines = (p.D * 2 + 127) / 128, heads = min(S::kRows, (kvh + 1) * p.group - h0);
+#pragma unroll 1
+        for (int i = lane; i < heads * lines; i += 32) {
+          const int h = i / lines;
+          const char *q = static_cast<const char *>(p.q) + 2 * ((long long)ahead.b * p.q_tok + (long long)(h0 + h) * p.q_head) + (i - h * lines) * 128;
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(q));
+        }
+      }
+    }
+  };
+  long long off = 0, group[S::kTok / 8];   // byte offsets in K and in V: this lane's row, each 8 rows
+  bool ok = false, all = false;            // this lane's row is copied; every row is
+  // A copy instruction moves 32 pieces: kPer rows, or a part of one.
+  constexpr int kPer = S::kPieces <= 32 ? 32 / S::kPieces : 1, kParts = S::kPieces <= 32 ? 1 : S::kPieces / 32;
+  const int my_row = S::kPieces <= 32 ? lane / S::kPieces : 0, my_piece = S::kPieces <= 32 ? lane % S::kPieces : lane;
+  const uint32_t my_dst = my_row * S::kRow + ((my_piece ^ S::swz(my_row)) << 4);
+  const uint32_t tok_b = (uint32_t)p.tok_b;
+  const long long my_off = (long long)my_row * p.tok_b + my_piece * 16;
+  int on[kParts];
+#pragma unroll
+  for (int x = 0; x < kParts; ++x) on[x] = x * 512 + my_piece * 16 < p.D * ES;
+  int next = 0, slot_in = 0;   // copies are numbered K, V, K, V, ...
+  auto issue_next = [&]() {
+    const bool is_v = next & 1;
+    if (to_copy > 0) {
+      const char *base = is_v ? p.v : p.k;
+      if (!is_v) {
+        const int r = lane & (S::kTok - 1);
+        const bool good = (unsigned)now.page < (unsigned)p.num_pages;
+        if (!good) atomicCAS(p.err, 0u, MOE_DEV_ERR_BAD_PAGE);
+        off = (long long)now.kvh * p.head_b + (good ? (long long)now.page * p.page_b + (long long)now.in_page * p.tok_b : 0);
+        ok = good && r >= now.first && r < now.last;
+        all = p.groups_of_8 && __all_sync(kAll, ok);
+        if (p.groups_of_8) {
+#pragma unroll
+          for (int x = 0; x < S::kTok / 8; ++x) group[x] = __shfl_sync(kAll, off, 8 * x);
+        }
+      }
+      const uint32_t dst = ring + slot_in * S::kUnit;
+      const uint32_t to = dst + my_dst;   // its low bits hold the piece: slots are multiples of a row
+      if (all) {
+        // whole 8-token groups, each in one page: two additions and an XOR a copy
+#pragma unroll
+        for (int x = 0; x < S::kTok / 8; ++x) {
+          const char *from = base + group[x] + my_off;
+#pragma unroll
+          for (int r = 0; r < 8; r += kPer) {
+            const char *row = from + (unsigned long long)(tok_b * (uint32_t)r);
+#pragma unroll
+            for (int part = 0; part < kParts; ++part)
+              copy16_if((to ^ (uint32_t)(S::swz(r) << 4)) + (x * 8 + r) * S::kRow + part * 512, row + part * 512, on[part]);
+          }
+        }
+      } else if (p.groups_of_8) {
+        // a sequence's or a window's end: rows that are no keys become zeros (0 x NaN in a page's
+        // unused rows would reach the output)
+        const unsigned rows = __ballot_sync(kAll, ok);
+#pragma unroll 1
+        for (int x = 0; x < S::kTok / 8; ++x) {
+          const char *from = base + __shfl_sync(kAll, off, 8 * x) + my_off;
+#pragma unroll
+          for (int r = 0; r < 8; r += kPer) {
+            const bool row_ok = rows >> (x * 8 + r + my_row) & 1;
+            const char *row = row_ok ? from + (unsigned long long)(tok_b * (uint32_t)r) : base;
+#pragma unroll
+            for (int part = 0; part < kParts; ++part)
+              copy16((to ^ (uint32_t)(S::swz(r) << 4)) + (x * 8 + r) * S::kRow + part * 512, row + part * 512, row_ok && on[part]);
+          }
         }
       } else {
-        copy_commit();
+#pragma unroll 4
+        for (int j = 0; j < S::kUnit / 512; ++j) {
+          const int idx = j * 32 + lane, r = idx / S::kPieces, ch = idx % S::kPieces;
+          const long long ro = __shfl_sync(kAll, off, r);
+          const bool row_ok = __shfl_sync(kAll, (int)ok, r) && ch * 16 < p.D * ES;
+          copy16(dst + r * S::kRow + ((ch ^ S::swz(r)) << 4), row_ok ? base + ro + ch * 16 : base, row_ok);
+        }
       }
-      ++next;
-      slot_in = slot_in + 1 == S::kUnits ? 0 : slot_in + 1;
-    };
-    look_up(0);
-    for (int i = 0; i < S::kUnits - 1; ++i) issue_next();
+      if (is_v) {
+        --to_copy;
+        now = then;
+        look_up(then);
+      }
+    }
+    copy_commit();
+    ++next;
+    slot_in = slot_in + 1 == S::kSlots ? 0 : slot_in + 1;
+  };
+  look_up(now);
+  then = now;
+  look_up(then);
 
-    // ---- q as B fragments: columns = heads, k = head elements
+  int4 rec = make_int4(0, 0, 0, 0);
+  int slot = 0, done = 0, lead = S::kSlots - 1;   // lead: copies issued before the first is waited for
+  while (true) {   // a piece: the units of one segment that are the warp's
+    const int kvh = at.seg / p.n_groups, h0 = kvh * p.group + (at.seg - kvh * p.n_groups) * S::kRows;
+    const int heads = min(S::kRows, (kvh + 1) * p.group - h0);
+    const int i0 = at.i, cnt = min(at.sp.n - i0, count - done);
+
     uint32_t qf[W / 16][NT][2];
     float sc[NT][2];   // score scale of the lane's two columns
+    auto load_q = [&]() {   // q as B fragments: columns = heads, k = head elements
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int hh = 8 * n + g;
-      const long long at = (long long)b * p.q_tok + (long long)(h0 + hh) * p.q_head;
-      if constexpr (ES == 2) {
-        const T *q = static_cast<const T *>(p.q) + at;
+      for (int n = 0; n < NT; ++n) {
+        const int hh = 8 * n + g;
+        const long long q_at = (long long)at.b * p.q_tok + (long long)(h0 + hh) * p.q_head;
+        if constexpr (ES == 2) {
+          const T *q = static_cast<const T *>(p.q) + q_at;
 #pragma unroll
-        for (int s = 0; s < W / 16; ++s)
+          for (int s = 0; s < W / 16; ++s)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int d = 16 * s + 8 * e + 2 * c;
-            qf[s][n][e] = hh < heads && d < p.D ? *reinterpret_cast<const uint32_t *>(q + d) : 0u;
+            for (int e = 0; e < 2; ++e) {
+              const int d = 16 * s + 8 * e + 2 * c;
+              qf[s][n][e] = hh < heads && d < p.D ? *reinterpret_cast<const uint32_t *>(q + d) : 0u;
+            }
+          sc[n][0] = sc[n][1] = p.scale_log2;
+        } else {
+          // k index of the e4m3 fragments: b0 holds elements 4c, 4c + 1 of the 16, b1 4c + 2, 4c + 3.
+          // q is scaled by a power of two that puts the head's largest value in [1, 2), so that
+          // fp16 holds a bf16 q; the scores are multiplied back.
+          float top = 0.f;
+          uint2 raw[W / 16];
+#pragma unroll
+          for (int s = 0; s < W / 16; ++s) {
+            const int d = 16 * s + 4 * c;
+            raw[s] = make_uint2(0u, 0u);
+            if (hh < heads && d < p.D) raw[s] = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.q) + q_at + d);
           }
-        sc[n][0] = sc[n][1] = p.scale_log2;
-      } else {
-        // k index of the e4m3 fragments: b0 holds elements 4c, 4c + 1 of the 16, b1 4c + 2, 4c + 3.
-        // q is scaled by a power of two that puts the head's largest value in [1, 2), so that
-        // fp16 holds a bf16 q; the scores are multiplied back.
-        float top = 0.f;
-        uint2 raw[W / 16];
+          auto up = [&](uint32_t w, float &x, float &y) {
+            if constexpr (QB) {
+              x = __uint_as_float(w << 16);
+              y = __uint_as_float(w & 0xffff0000u);
+            } else {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+              x = f.x;
+              y = f.y;
+            }
+          };
 #pragma unroll
-        for (int s = 0; s < W / 16; ++s) {
-          const int d = 16 * s + 4 * c;
-          raw[s] = make_uint2(0u, 0u);
-          if (hh < heads && d < p.D) raw[s] = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.q) + at + d);
-        }
-        auto up = [&](uint32_t w, float &x, float &y) {
-          if constexpr (QB) {
-            x = __uint_as_float(w << 16);
-            y = __uint_as_float(w & 0xffff0000u);
-          } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-            x = f.x;
-            y = f.y;
+          for (int s = 0; s < W / 16; ++s) {
+            float x, y;
+            up(raw[s].x, x, y);
+            top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+            up(raw[s].y, x, y);
+            top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
           }
-        };
+          top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+          int eb = (int)(__float_as_uint(top) >> 23);          // biased exponent
+          eb = eb < 1 ? 127 : (eb > 253 ? 253 : eb);
+          const float down = __uint_as_float((uint32_t)(254 - eb) << 23), back = __uint_as_float((uint32_t)eb << 23);
 #pragma unroll
-        for (int s = 0; s < W / 16; ++s) {
-          float x, y;
-          up(raw[s].x, x, y);
-          top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
-          up(raw[s].y, x, y);
-          top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+          for (int s = 0; s < W / 16; ++s) {
+            float x, y;
+            up(raw[s].x, x, y);
+            qf[s][n][0] = M::pack(x * down, y * down);
+            up(raw[s].y, x, y);
+            qf[s][n][1] = M::pack(x * down, y * down);
+          }
+          sc[n][0] = p.scale_log2 * __shfl_sync(kAll, back, 8 * c);
+          sc[n][1] = p.scale_log2 * __shfl_sync(kAll, back, 8 * c + 4);
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int eb = (int)(__float_as_uint(top) >> 23);          // biased exponent
-        eb = eb < 1 ? 127 : (eb > 253 ? 253 : eb);
-        const float down = __uint_as_float((uint32_t)(254 - eb) << 23), back = __uint_as_float((uint32_t)eb << 23);
-#pragma unroll
-        for (int s = 0; s < W / 16; ++s) {
-          float x, y;
-          up(raw[s].x, x, y);
-          qf[s][n][0] = M::pack(x * down, y * down);
-          up(raw[s].y, x, y);
-          qf[s][n][1] = M::pack(x * down, y * down);
-        }
-        sc[n][0] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * c);
-        sc[n][1] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * c + 4);
       }
-    }
-
+    };
     float o[W / 16][NT][4];
 #pragma unroll
     for (int s = 0; s < W / 16; ++s)
@@ -350,290 +545,312 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const AttnParams p)
         for (int e = 0; e < 4; ++e) o[s][n][e] = 0.f;
     float mx[NT][2], l[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = __int_as_float(0xff800000), l[n][0] = l[n][1] = 0.f;
+    for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = ninf, l[n][0] = l[n][1] = 0.f;
 
-    int slot = 0;
-    for (int i = 0; i < cnt; ++i) {
-      // ---- S^T = K Q^T
-      copy_wait<S::kUnits - 2>();
-      __syncwarp();
-      float s[NT][2][4];   // two accumulators shorten the chain
+    int t0 = at.token();
+    uint32_t pf[S::kTiles][NT][2];   // P^T as B fragments
+    // One step a copy: K, V, K, V, ... (a single place that issues copies keeps the code small
+    // enough for the instruction cache)
+#pragma unroll 1
+    for (int step = -lead; step < 2 * cnt; ++step) {
+      if (step >= 0) {
+        if (step == 0) load_q();
+        copy_wait<S::kSlots - 2>();
+        __syncwarp();
+        const uint32_t unit = ring + slot * S::kUnit;
+        if (!(step & 1)) {
+          // ---- S^T = K Q^T
+          constexpr int kAcc = S::kTiles == 1 ? 2 : 1;   // a single row tile takes two accumulators, to shorten the chain
+          float s[S::kTiles][NT][kAcc][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+          for (int t = 0; t < S::kTiles; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][0][e] = s[n][1][e] = 0.f;
-      {
-        const uint32_t ku = ring + slot * S::kUnit;
-        const int r = (lane & 7) + (lane & 8), hi = lane >> 4;
-        const uint32_t base = ku + r * S::kRow;
-        const int x = S::swz(r);
-        if constexpr (ES == 2) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int k = 0; k < W / 16; ++k) {
-            uint32_t a[4];
-            ldsm4(a, base + (((2 * k + hi) ^ x) << 4));
+              for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) M::run(s[n][k & 1], a, qf[k][n][0], qf[k][n][1]);
+                for (int x = 0; x < kAcc; ++x) s[t][n][x][e] = 0.f;
+          {
+                    const int r = (lane & 7) + (lane & 8), hi = lane >> 4;
+            const uint32_t base = unit + r * S::kRow + ((hi ^ S::swz(r)) << 4);
+            if constexpr (ES == 2) {
+#pragma unroll
+              for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+                for (int t = 0; t < S::kTiles; ++t) {
+                  uint32_t a[4];
+                  ldsm4(a, S::at(base, k) + t * 16 * S::kRow);
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) M::run(s[t][n][k & (kAcc - 1)], a, qf[k][n][0], qf[k][n][1]);
+                }
+            } else {
+#pragma unroll
+              for (int k = 0; k < W / 32; ++k)
+#pragma unroll
+                for (int t = 0; t < S::kTiles; ++t) {
+                  uint32_t w[4];
+                  ldsm4(w, S::at(base, k) + t * 16 * S::kRow);
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    uint32_t a[4];
+                    a[0] = e4m3x2_to_f16x2(w[2 * h]);
+                    a[1] = e4m3x2_to_f16x2(w[2 * h + 1]);
+                    a[2] = e4m3x2_to_f16x2(w[2 * h] >> 16);
+                    a[3] = e4m3x2_to_f16x2(w[2 * h + 1] >> 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) M::run(s[t][n][h & (kAcc - 1)], a, qf[2 * k + h][n][0], qf[2 * k + h][n][1]);
+                  }
+                }
+            }
+          }
+
+          // ---- softmax over the unit's tokens, in base 2
+          const bool full = t0 >= at.sp.lo && t0 + S::kTok <= at.sp.len;   // every token of the unit is a key
+          bool scale_o = false;
+          float al[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float v[S::kTiles][4];
+#pragma unroll
+            for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[t][e] = (kAcc == 2 ? s[t][n][0][e] + s[t][n][kAcc - 1][e] : s[t][n][0][e]) * sc[n][e & 1];
+            if (!full) {
+#pragma unroll
+              for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int tok = t0 + g + 16 * t + 8 * (e >> 1);
+                  if (tok < at.sp.lo || tok >= at.sp.len) v[t][e] = ninf;
+                }
+            }
+            float m0 = fmaxf(v[0][0], v[0][2]), m1 = fmaxf(v[0][1], v[0][3]);
+#pragma unroll
+            for (int t = 1; t < S::kTiles; ++t) {
+              m0 = fmaxf(m0, fmaxf(v[t][0], v[t][2]));
+              m1 = fmaxf(m1, fmaxf(v[t][1], v[t][3]));
+            }
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+              m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
+              m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
+            }
+            m0 = fmaxf(m0, mx[n][0]);
+            m1 = fmaxf(m1, mx[n][1]);
+            // a maximum of -inf (no key yet) must not meet itself in a difference
+            const float b0 = (m0 == ninf ? 0.f : m0) - M::kOff, b1 = (m1 == ninf ? 0.f : m1) - M::kOff;
+            al[n][0] = exp2_fast(mx[n][0] - M::kOff - b0);
+            al[n][1] = exp2_fast(mx[n][1] - M::kOff - b1);
+            scale_o |= m0 != mx[n][0] || m1 != mx[n][1];
+            mx[n][0] = m0;
+            mx[n][1] = m1;
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int t = 0; t < S::kTiles; ++t) {
+              const float p0 = exp2_fast(v[t][0] - b0), p1 = exp2_fast(v[t][1] - b1), p2 = exp2_fast(v[t][2] - b0), p3 = exp2_fast(v[t][3] - b1);
+              s0 += p0 + p2;
+              s1 += p1 + p3;
+              pf[t][n][0] = transposed8x8(M::pack(p0, p1));
+              pf[t][n][1] = transposed8x8(M::pack(p2, p3));
+            }
+            l[n][0] = fmaf(l[n][0], al[n][0], s0);
+            l[n][1] = fmaf(l[n][1], al[n][1], s1);
+          }
+          if (__any_sync(0xffffffffu, scale_o)) {
+#pragma unroll
+            for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                o[k][n][0] *= al[n][0];
+                o[k][n][1] *= al[n][1];
+                o[k][n][2] *= al[n][0];
+                o[k][n][3] *= al[n][1];
+              }
           }
         } else {
+          // ---- O^T += V^T P^T
+          {
+                    if constexpr (ES == 2) {
+              const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
+              const uint32_t base = unit + r * S::kRow + ((hi ^ S::swz(r)) << 4);
 #pragma unroll
-          for (int k = 0; k < W / 32; ++k) {
-            uint32_t w[4];
-            ldsm4(w, base + (((2 * k + hi) ^ x) << 4));
-            uint32_t a[4];
-            a[0] = e4m3x2_to_f16x2(w[0]);
-            a[1] = e4m3x2_to_f16x2(w[1]);
-            a[2] = e4m3x2_to_f16x2(w[0] >> 16);
-            a[3] = e4m3x2_to_f16x2(w[1] >> 16);
+              for (int t = 0; t < S::kTiles; ++t)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) M::run(s[n][0], a, qf[2 * k][n][0], qf[2 * k][n][1]);
-            a[0] = e4m3x2_to_f16x2(w[2]);
-            a[1] = e4m3x2_to_f16x2(w[3]);
-            a[2] = e4m3x2_to_f16x2(w[2] >> 16);
-            a[3] = e4m3x2_to_f16x2(w[3] >> 16);
+                for (int k = 0; k < W / 16; ++k) {
+                  uint32_t a[4];
+                  ldsm4t(a, S::at(base, k) + t * 16 * S::kRow);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) M::run(s[n][1], a, qf[2 * k + 1][n][0], qf[2 * k + 1][n][1]);
+                  for (int n = 0; n < NT; ++n) M::run(o[k][n], a, pf[t][n][0], pf[t][n][1]);
+                }
+            } else {
+              const int r = (lane & 7) + (lane & 8), hi = lane >> 4;
+              const uint32_t base = unit + r * S::kRow + ((hi ^ S::swz(r)) << 4);
+#pragma unroll
+              for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+                for (int k = 0; k < W / 32; ++k) {
+                  uint32_t w[4];
+                  ldsm4t(w, S::at(base, k) + t * 16 * S::kRow);
+                  // a word holds elements (2g, 2g + 1) of token 2c, then of token 2c + 1: row g of the
+                  // product's tile takes element 2g, row g + 8 element 2g + 1
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t lo = __byte_perm(w[2 * h], 0u, 0x3120), hi8 = __byte_perm(w[2 * h + 1], 0u, 0x3120);
+                    uint32_t a[4];
+                    a[0] = e4m3x2_to_f16x2(lo);
+                    a[1] = e4m3x2_to_f16x2(lo >> 16);
+                    a[2] = e4m3x2_to_f16x2(hi8);
+                    a[3] = e4m3x2_to_f16x2(hi8 >> 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) M::run(o[2 * k + h][n], a, pf[t][n][0], pf[t][n][1]);
+                  }
+                }
+            }
           }
+          t0 += S::kTok;
         }
+        slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+        __syncwarp();
       }
-      slot = slot + 1 == S::kUnits ? 0 : slot + 1;
-      __syncwarp();
       issue_next();
+    }
+    lead = 0;
 
-      // ---- softmax over the unit's tokens, in base 2
-      const int t0 = t_first + i * MOE_ATTN_CHUNK + g;
-      const bool in0 = t0 >= sp.lo && t0 < sp.len, in1 = t0 + 8 >= sp.lo && t0 + 8 < sp.len;
-      uint32_t pf[NT][2];
-      bool scale_o = false;
-      float al[NT][2];
+    // ---- the piece's result
+    done += cnt;
+    const bool whole = cnt == at.sp.n;
+    float inv[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(kAll, l[n][e], x);
+        inv[n][e] = l[n][e] == 0.f ? 0.f : p.v_scale / l[n][e];
+      }
+    if (whole) {
+      TO *out = static_cast<TO *>(p.out) + (long long)at.b * p.out_tok + (long long)h0 * p.out_head;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float ninf = __int_as_float(0xff800000);
-        const float v0 = in0 ? (s[n][0][0] + s[n][1][0]) * sc[n][0] : ninf, v1 = in0 ? (s[n][0][1] + s[n][1][1]) * sc[n][1] : ninf;
-        const float v2 = in1 ? (s[n][0][2] + s[n][1][2]) * sc[n][0] : ninf, v3 = in1 ? (s[n][0][3] + s[n][1][3]) * sc[n][1] : ninf;
-        float m0 = fmaxf(v0, v2), m1 = fmaxf(v1, v3);
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
-          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
+        for (int k = 0; k < W / 16; ++k)
+          if (16 * k < p.D)
+            store_fragment<TO, ES>(out + 8 * n * p.out_head, p.out_head, k, heads - 8 * n, lane,
+                                   make_float4(o[k][n][0], o[k][n][1], o[k][n][2], o[k][n][3]), inv[n][0], inv[n][1]);
+        if (p.lse && g == 0) {
+          float *lse = p.lse + (long long)at.b * p.nq + h0 + 8 * n + 2 * c;
+          if (8 * n + 2 * c < heads) lse[0] = (mx[n][0] + (log2f(l[n][0]) - M::kOff)) * kLn2;
+          if (8 * n + 2 * c + 1 < heads) lse[1] = (mx[n][1] + (log2f(l[n][1]) - M::kOff)) * kLn2;
         }
-        m0 = fmaxf(m0, mx[n][0]);
-        m1 = fmaxf(m1, mx[n][1]);
-        // a maximum of -inf (no key yet) must not meet itself in a difference
-        const float b0 = (m0 == ninf ? 0.f : m0) - M::kOff, b1 = (m1 == ninf ? 0.f : m1) - M::kOff;
-        al[n][0] = exp2_fast(mx[n][0] - M::kOff - b0);
-        al[n][1] = exp2_fast(mx[n][1] - M::kOff - b1);
-        scale_o |= m0 != mx[n][0] || m1 != mx[n][1];
-        mx[n][0] = m0;
-        mx[n][1] = m1;
-        const float p0 = exp2_fast(v0 - b0), p1 = exp2_fast(v1 - b1), p2 = exp2_fast(v2 - b0), p3 = exp2_fast(v3 - b1);
-        l[n][0] = l[n][0] * al[n][0] + (p0 + p2);
-        l[n][1] = l[n][1] * al[n][1] + (p1 + p3);
-        pf[n][0] = transposed8x8(M::pack(p0, p1));
-        pf[n][1] = transposed8x8(M::pack(p2, p3));
       }
-      if (__any_sync(0xffffffffu, scale_o)) {
+    } else {
+      const int w0 = split.owner(seg_first + extra), w1 = split.owner(seg_first + extra + at.sp.n - 1);
+      float4 *ws = reinterpret_cast<float4 *>(p.ws_o), *ws_ml = reinterpret_cast<float4 *>(p.ws_ml);
+      if (extra && Block(blockIdx.x).inside(w0, w1)) {
+        // the block's four warps have nothing but parts of this segment: one piece of them
+        __shared__ float4 sh_ml[kWarps][4 * NT];
+        float4 *mine = reinterpret_cast<float4 *>(smem + warp * (S::kSlots * S::kUnit)) + lane;
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < W / 16; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            o[k][n][0] *= al[n][0];
-            o[k][n][1] *= al[n][1];
-            o[k][n][2] *= al[n][0];
-            o[k][n][3] *= al[n][1];
+          for (int n = 0; n < NT; ++n) mine[(k * NT + n) * 32] = make_float4(o[k][n][0], o[k][n][1], o[k][n][2], o[k][n][3]);
+        if (g == 0) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sh_ml[warp][4 * n + c] = make_float4(mx[n][0], l[n][0], mx[n][1], l[n][1]);
+        }
+        __syncthreads();
+        const long long piece = 2ll * blockIdx.x * kWarps;
+#pragma unroll 1
+        for (int f = warp; f < p.D / 16 * NT; f += kWarps) {
+          Joined j;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w)
+            j.take(sh_ml[w][4 * (f % NT) + c], reinterpret_cast<const float4 *>(smem + w * (S::kSlots * S::kUnit))[f * 32 + lane]);
+          ws[piece * (p.D / 16 * NT * 32) + f * 32 + lane] = j.acc;
+          if (f < NT && g == 0) ws_ml[piece * (4 * NT) + 4 * f + c] = j.ml;
+        }
+      } else {
+        // slot 0: a segment that came in from the worker before; slot 1: one that starts here
+        const long long piece = 2ll * worker + (i0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int k = 0; k < W / 16; ++k)
+          if (16 * k < p.D) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              ws[piece * (p.D / 16 * NT * 32) + (k * NT + n) * 32 + lane] = make_float4(o[k][n][0], o[k][n][1], o[k][n][2], o[k][n][3]);
           }
-      }
-
-      // ---- O^T += V^T P^T
-      copy_wait<S::kUnits - 2>();
-      __syncwarp();
-      {
-        const uint32_t vu = ring + slot * S::kUnit;
-        if constexpr (ES == 2) {
-          const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
-          const uint32_t base = vu + r * S::kRow;
-          const int x = S::swz(r);
+        if (g == 0) {
 #pragma unroll
-          for (int k = 0; k < W / 16; ++k) {
-            uint32_t a[4];
-            ldsm4t(a, base + (((2 * k + hi) ^ x) << 4));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) M::run(o[k][n], a, pf[n][0], pf[n][1]);
-          }
-        } else {
-          const int r = (lane & 7) + (lane & 8), hi = lane >> 4;
-          const uint32_t base = vu + r * S::kRow;
-          const int x = S::swz(r);
-#pragma unroll
-          for (int k = 0; k < W / 32; ++k) {
-            uint32_t w[4];
-            ldsm4t(w, base + (((2 * k + hi) ^ x) << 4));
-            // a word holds elements (2g, 2g + 1) of token 2c, then of token 2c + 1: row g of the
-            // product's tile takes element 2g, row g + 8 element 2g + 1
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t lo = __byte_perm(w[2 * h], 0u, 0x3120), hi8 = __byte_perm(w[2 * h + 1], 0u, 0x3120);
-              uint32_t a[4];
-              a[0] = e4m3x2_to_f16x2(lo);
-              a[1] = e4m3x2_to_f16x2(lo >> 16);
-              a[2] = e4m3x2_to_f16x2(hi8);
-              a[3] = e4m3x2_to_f16x2(hi8 >> 16);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) M::run(o[2 * k + h][n], a, pf[n][0], pf[n][1]);
-            }
-          }
+          for (int n = 0; n < NT; ++n) ws_ml[piece * (4 * NT) + 4 * n + c] = make_float4(mx[n][0], l[n][0], mx[n][1], l[n][1]);
         }
       }
-      slot = slot + 1 == S::kUnits ? 0 : slot + 1;
-      __syncwarp();
-      issue_next();
+      if (i0 == 0) rec = make_int4(worker + 1, at.b, at.seg, w1 | (extra << 30));
     }
-
-    // ---- join the four warps
-    copy_wait<0>();
-    __syncthreads();
-    float *jo = reinterpret_cast<float *>(smem);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) {
-        l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], x);
-        l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], x);
-      }
-      if (g == 0) {
-        sh_m[warp][8 * n + 2 * c] = mx[n][0];
-        sh_m[warp][8 * n + 2 * c + 1] = mx[n][1];
-        sh_l[warp][8 * n + 2 * c] = l[n][0];
-        sh_l[warp][8 * n + 2 * c + 1] = l[n][1];
-      }
-      float *w0 = jo + (warp * S::kRows + 8 * n + 2 * c) * S::kPitch, *w1 = w0 + S::kPitch;
-#pragma unroll
-      for (int k = 0; k < W / 16; ++k) {
-        const int d0 = ES == 2 ? 16 * k + g : 16 * k + 2 * g, d1 = ES == 2 ? d0 + 8 : d0 + 1;
-        w0[d0] = o[k][n][0];
-        w1[d0] = o[k][n][1];
-        w0[d1] = o[k][n][2];
-        w1[d1] = o[k][n][3];
-      }
-    }
-    __syncthreads();
-    const bool whole = cnt == sp.n;
-    const int piece = 2 * (int)cta + (i0 == 0 ? 1 : 0);
-    for (int i = tid; i < heads * (p.D / 2); i += kWarps * 32) {
-      const int h = i / (p.D / 2), d = 2 * (i - h * (p.D / 2));
-      float m = sh_m[0][h];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh_m[w][h]);
-      const float base = m == __int_as_float(0xff800000) ? 0.f : m;
-      float sum = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_fast(sh_m[w][h] - base);
-        const float2 v = *reinterpret_cast<const float2 *>(jo + (w * S::kRows + h) * S::kPitch + d);
-        sum = fmaf(f, sh_l[w][h], sum);
-        x = fmaf(f, v.x, x);
-        y = fmaf(f, v.y, y);
-      }
-      if (whole) {
-        const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-        const long long at = (long long)b * p.out_tok + (long long)(h0 + h) * p.out_head + d;
-        if constexpr (ES == 1 && QB)
-          *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.out) + at) = Mma<__nv_bfloat16>::pack(x * inv, y * inv);
-        else
-          *reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at) = M::pack(x * inv, y * inv);
-        if (p.lse && d == 0) p.lse[(long long)b * p.nq + h0 + h] = (m + (log2f(sum) - M::kOff)) * kLn2;
-      } else {
-        const long long at = (long long)piece * S::kRows + h;
-        *reinterpret_cast<float2 *>(p.ws_o + at * p.D + d) = make_float2(x, y);
-        if (d == 0) p.ws_ml[at] = make_float2(m, sum);
-      }
-    }
-    __syncthreads();
-
-    if (!whole && i0 == 0) {   // the segment starts here and goes on: its last chunk's CTA
-      const long long e = seq_first * hs + (long long)(seg + 1) * sp.n;
-      rec = make_int4(1, b, seg, (int)((e * ctas - 1) / total));
-    }
-    u += cnt;
-    if (u < u_end && u >= (seq_first + sp.n) * hs) {
-      seq_first += sp.n;
-      do sp = span_of(p, ++b);
-      while (sp.n == 0);
-    }
+    if (i0 == 0 && p.rec_by_segment && lane == 0) p.rec[at.b * segs + at.seg] = whole ? make_int4(0, 0, 0, 0) : rec;
+    if (done == count) break;
+    seg_first += at.sp.n + extra;
+    at.i = at.sp.n - 1;
+    at.next(p, segs);
   }
-  if (tid == 0) p.rec[blockIdx.x] = rec;
+  if (!p.rec_by_segment && lane == 0) p.rec[worker] = rec;
 }
 
-// Sums the pieces of the segment that starts in CTA blockIdx.x and ends in a later one:
-// row blockIdx.y of its heads. 256 threads: a float4 of the row each, several pieces at a time.
-template <typename TO>
-__global__ void __launch_bounds__(256) k_attn_join(const AttnParams p, int rows, float off) {
-  __shared__ float sw[MOE_ATTN_MAX_CTAS];
-  __shared__ float sred[8], ssum[8];
-  __shared__ float4 sacc[256];
+// Sums the pieces of record blockIdx.x's segment. A thread takes one fragment of a piece (two heads
+// at two elements: four values), of every par-th piece (the block's threads are par groups over the
+// same threads / par fragments), and joins them as it goes, so that only the record is waited for
+// before the pieces' loads; then the groups are joined pairwise through shared memory.
+constexpr int kJoinMost = 512;   // threads
+template <typename TO, int ES>
+__global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int nt, int par, float off) {
+  __shared__ float4 s_acc[kJoinMost / 2], s_ml[kJoinMost / 2];
   pdl_wait();
   const int4 rec = p.rec[blockIdx.x];
   if (!rec.x) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = rec.y, kvh = rec.z / p.n_groups, h = kvh * p.group + (rec.z - kvh * p.n_groups) * rows + blockIdx.y;
-  if (h >= (kvh + 1) * p.group) return;
-  const int c0 = blockIdx.x, n = rec.w - c0 + 1;
-  // piece j: the starting CTA's second slot, then the later CTAs' first slots
-  auto at = [&](int j) { return (long long)(2 * (c0 + j) + (j == 0 ? 1 : 0)) * rows + blockIdx.y; };
-  const float ninf = __int_as_float(0xff800000);
-  float m = ninf;
-  for (int j = tid; j < n; j += 256) m = fmaxf(m, p.ws_ml[at(j)].x);
+  const int tid = threadIdx.x, lane = tid & 31, per = blockDim.x / par, j0 = tid / per;   // per: a multiple of 32
+  const int frags = p.D / 16 * nt * 32, f = blockIdx.y * per + (tid - j0 * per);
+  const int k = f / (32 * nt), n = f / 32 - k * nt, c = lane & 3;
+  const int b = rec.y, kvh = rec.z / p.n_groups, h0 = kvh * p.group + (rec.z - kvh * p.n_groups) * 8 * nt + 8 * n;
+  const int heads = (kvh + 1) * p.group - h0;   // that exist from this column tile on
+  const Pieces pieces(rec.x - 1, rec.w & 0x3fffffff, rec.w >> 30);
+  Joined sum;
+  if (f < frags) {
+    constexpr int kAhead = 4;
+    const float4 *po = reinterpret_cast<const float4 *>(p.ws_o) + f, *pm = reinterpret_cast<const float4 *>(p.ws_ml) + (4 * n + c);
+    for (int j = j0; j < pieces.count; j += kAhead * par) {
+      float4 m[kAhead], v[kAhead];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) sred[warp] = m;
-  __syncthreads();
+      for (int x = 0; x < kAhead; ++x) {
+        const int i = j + x * par;
+        if (i >= pieces.count) continue;
+        // piece 0: the starting worker's second slot; then the later workers' first slots
+        const long long at = 2ll * pieces.worker(i) + (i == 0 ? 1 : 0);
+        m[x] = pm[at * (4 * nt)];
+        v[x] = po[at * frags];
+      }
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m = fmaxf(m, sred[w]);
-  const float base = m == ninf ? 0.f : m;
-  float sum = 0.f;
-  for (int j = tid; j < n; j += 256) {
-    const float2 ml = p.ws_ml[at(j)];
-    const float f = exp2_fast(ml.x - base);
-    sw[j] = f;
-    sum = fmaf(f, ml.y, sum);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) ssum[warp] = sum;
-  __syncthreads();
-  sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) sum += ssum[w];
-
-  const int quads = p.D / 4, par = 256 / quads, j0 = tid / quads, q = tid - j0 * quads;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (j0 < par) {
-#pragma unroll 4
-    for (int j = j0; j < n; j += par) {
-      const float4 v = *reinterpret_cast<const float4 *>(p.ws_o + at(j) * p.D + 4 * q);
-      const float f = sw[j];
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
+      for (int x = 0; x < kAhead; ++x)
+        if (j + x * par < pieces.count) sum.take(m[x], v[x]);
     }
   }
-  sacc[tid] = acc;
-  __syncthreads();
-  if (tid < quads) {
-    for (int j = 1; j < par; ++j) {
-      const float4 v = sacc[j * quads + tid];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
+  for (int half = par >> 1; half; half >>= 1) {
+    __syncthreads();
+    if (j0 >= half && j0 < 2 * half) {
+      s_acc[tid - half * per] = sum.acc;
+      s_ml[tid - half * per] = sum.ml;
     }
-    const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-    uint2 w;
-    w.x = Mma<TO>::pack(acc.x * inv, acc.y * inv);
-    w.y = Mma<TO>::pack(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2 *>(static_cast<TO *>(p.out) + (long long)b * p.out_tok + (long long)h * p.out_head + 4 * tid) = w;
-    if (p.lse && tid == 0) p.lse[(long long)b * p.nq + h] = (m + (log2f(sum) - off)) * kLn2;
+    __syncthreads();
+    if (j0 < half) sum.take(s_ml[tid], s_acc[tid]);
+  }
+  if (j0 || f - lane >= frags) return;   // whole warps
+  TO *out = static_cast<TO *>(p.out) + (long long)b * p.out_tok + (long long)h0 * p.out_head;
+  store_fragment<TO, ES>(out, p.out_head, k, heads, lane, sum.acc, sum.ml.y == 0.f ? 0.f : p.v_scale / sum.ml.y,
+                           sum.ml.w == 0.f ? 0.f : p.v_scale / sum.ml.w);
+  if (p.lse && k == 0 && lane < 4) {
+    float *lse = p.lse + (long long)b * p.nq + h0 + 2 * c;
+    if (2 * c < heads) lse[0] = (sum.ml.x + (log2f(sum.ml.y) - off)) * kLn2;
+    if (2 * c + 1 < heads) lse[1] = (sum.ml.z + (log2f(sum.ml.w) - off)) * kLn2;
   }
 }
 
@@ -650,19 +867,34 @@ template <typename T, int W, int NT, int ES, bool QB> int launch(const AttnParam
     __atomic_store_n(&per_sm, occ, __ATOMIC_RELAXED);
   }
   int grid = num_sms * occ;
-  if (grid > MOE_ATTN_MAX_CTAS) grid = MOE_ATTN_MAX_CTAS;
-  fn<<<grid, kWarps * 32, S::kSmem, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return -1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, S::kRows < p.group ? S::kRows : p.group);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
+  if (grid * kWarps > MOE_ATTN_MAX_WORKERS) grid = MOE_ATTN_MAX_WORKERS / kWarps;
+  AttnParams a = p;
+  // A record a segment where there are fewer segments than workers, else a record a worker: the
+  // join's grid is as small as can be said without the lengths
+  const long long segments = (long long)p.B * p.nkv * p.n_groups;
+  const int workers = grid * kWarps;
+  a.rec_by_segment = segments <= workers;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, k_attn_join<TO>, p, S::kRows, Mma<T>::kOff) != cudaSuccess) return -1;
+  if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) return -1;
+  // Threads that share a fragment in the join: as many as a quarter of the pieces that a segment
+  // has when all are equally long and blocks join theirs, so that each one's loads are in flight
+  // together
+  int par = 1;
+  while (par < 16 && 4 * par * segments < grid) par *= 2;
+  const int threads = par > 4 ? kJoinMost : kJoinMost / 2, frags = p.D / 16 * NT * 32, per = threads / par;
+  cfg.gridDim = dim3(a.rec_by_segment ? (unsigned)segments : workers, (frags + per - 1) / per);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = 0;
+  if (cudaLaunchKernelEx(&cfg, k_attn_join<TO, ES>, a, NT, par, Mma<T>::kOff) != cudaSuccess) return -1;
   moe_prof_count(2);
   return 0;
 }

@@ -16,6 +16,8 @@
 // work through shared memory.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "moe_attn.cuh"
 
 namespace {
@@ -62,7 +64,7 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&v)[8], float scale) {
 
 // lanes: lanes of a head (a power of two); split: warps that share a token's heads.
 template <typename T, bool INTER, bool F8>
-__global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const RopeParams p, int lanes, int split) {
+__global__ void __launch_bounds__(kThreads, 3) k_qk_norm_rope(const __grid_constant__ RopeParams p, int lanes, int split) {
   extern __shared__ float2 sh_turn[];   // [warps][rot / 2] cos, sin
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned work = blockIdx.x * kWarpsPerCta + warp;   // below T + 16 SMs: fits
@@ -77,41 +79,18 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const RopeParams p, i
   // the lane's two pieces of a head, and whether they turn
   const int half = p.rot / 2;
   int ea = 16 * sub, eb = ea + 8;
-  bool turns = ea < p.rot;
+  const bool turns = ea < p.rot;
   if (!INTER && turns) {
     ea = 8 * sub;
     eb = ea + half;
   }
   const bool in = 16 * sub < p.D;
 
-  auto source = [&](int i, bool &ok) -> const T * {
-    if (i < pq) {
-      const int h = i * per + grp;
-      ok = in && h < p.nq;
-      return static_cast<const T *>(p.q) + (long long)t * p.q_tok + (long long)h * p.q_head;
-    }
-    const bool is_v = i >= pq + pk;
-    const int h = (i - pq - (is_v ? pk : 0)) * per + grp;
-    ok = in && h < p.nkv;
-    return is_v ? static_cast<const T *>(p.v) + (long long)t * p.v_tok + (long long)h * p.v_head
-                : static_cast<const T *>(p.k) + (long long)t * p.k_tok + (long long)h * p.k_head;
-  };
-  uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
-  auto load = [&](int i) {
-    bool ok;
-    const T *src = source(i, ok);
-    if (ok) {
-      ra = *reinterpret_cast<const uint4 *>(src + ea);
-      rb = *reinterpret_cast<const uint4 *>(src + eb);
-    } else {
-      ra = rb = make_uint4(0, 0, 0, 0);
-    }
-  };
-  if (i0 < i1) load(i0);
-
   // cosines and sines of the lane's 8 pairs
   float cs[8], sn[8];
-  if (p.rot && i0 < pq + pk) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) cs[j] = 1.f, sn[j] = 0.f;
+  auto angles = [&]() {
     float2 *turn = sh_turn + warp * half;
     const double pos = (double)p.positions[t];
     for (int i = lane; i < half; i += 32) {
@@ -125,52 +104,78 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const RopeParams p, i
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = (INTER ? ea / 2 : ea) + j;
-      const float2 v = turns && i < half ? turn[i] : make_float2(1.f, 0.f);
-      cs[j] = v.x;
-      sn[j] = v.y;
+      if (turns && i < half) {
+        const float2 v = turn[i];
+        cs[j] = v.x;
+        sn[j] = v.y;
+      }
     }
-  }
+  };
 
-  long long slot = -1;
-  if (p.ck) {
-    slot = p.slots[t];
+  long long row = -1;   // the token's place in the cache, bytes
+  if (p.ck && i1 > pq) {
+    const long long slot = p.slots[t];
     if (slot >= p.n_slots) {
       report_error(p.err, MOE_DEV_ERR_BAD_SLOT, 0);
-      slot = -1;
+    } else if (slot >= 0) {
+      const long long page = slot >> 32 ? slot / p.page_size : (long long)((unsigned)slot / (unsigned)p.page_size);
+      row = page * p.page_b + (slot - page * p.page_size) * p.tok_b;
     }
   }
-  long long row = 0;
-  if (slot >= 0) {
-    const long long page = slot >> 32 ? slot / p.page_size : (long long)((unsigned)slot / (unsigned)p.page_size);
-    row = page * p.page_b + (slot - page * p.page_size) * p.tok_b;
-  }
 
-  const float *gain_now = nullptr;
-  float ga[8], gb[8];
-  for (int i = i0; i < i1; ++i) {
-    bool ok;
-    source(i, ok);
-    float a[8], b[8];
-    unpack8<T>(ra, a);
-    unpack8<T>(rb, b);
-    if (i + 1 < i1) load(i + 1);
-    const bool is_q = i < pq, is_v = i >= pq + pk;
-    const int h = (i - (is_q ? 0 : is_v ? pq + pk : pq)) * per + grp;
-    if (!is_v) {
-      const float *gain = is_q ? p.q_gain : p.k_gain;
-      if (gain) {
-        if (gain != gain_now && in) {
-          gain_now = gain;
+  // Passes [from, to) of one kind of heads (kind 0: q, 1: k, 2: v). The next pass's loads are in
+  // flight while one is computed; the first ones while the angles are.
+  bool have_angles = false;
+  auto heads_of = [&](auto kind_c, int from, int to, const T *src, long long src_head, int n, const float *gain, T *out,
+                      long long out_head, char *cache, float scale) {
+    constexpr int kind = decltype(kind_c)::value;
+    if (from >= to) return;
+    int h = from * per + grp;
+    src += (long long)h * src_head;
+    out += (long long)h * out_head;
+    cache += (long long)h * p.head_b;
+    uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+    auto load = [&]() {
+      if (in && h < n) {
+        ra = *reinterpret_cast<const uint4 *>(src + ea);
+        rb = *reinterpret_cast<const uint4 *>(src + eb);
+      }
+    };
+    load();
+    float ga[8], gb[8];
+    if (kind < 2 && gain) {
 #pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(gain + ea + j), y = *reinterpret_cast<const float4 *>(gain + eb + j);
-            ga[j] = x.x, ga[j + 1] = x.y, ga[j + 2] = x.z, ga[j + 3] = x.w;
-            gb[j] = y.x, gb[j + 1] = y.y, gb[j + 2] = y.z, gb[j + 3] = y.w;
-          }
+      for (int j = 0; j < 8; j += 4) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (in) {
+          x = *reinterpret_cast<const float4 *>(gain + ea + j);
+          y = *reinterpret_cast<const float4 *>(gain + eb + j);
         }
-        float ss = 0.f;
+        ga[j] = x.x, ga[j + 1] = x.y, ga[j + 2] = x.z, ga[j + 3] = x.w;
+        gb[j] = y.x, gb[j + 1] = y.y, gb[j + 2] = y.z, gb[j + 3] = y.w;
+      }
+    }
+    if (kind < 2 && p.rot && !have_angles) {
+      angles();
+      have_angles = true;
+    }
+#pragma unroll 1
+    for (int i = from; i < to; ++i) {
+      const bool ok = in && h < n;
+      float a[8], b[8];
+      unpack8<T>(ra, a);
+      unpack8<T>(rb, b);
+      h += per;
+      src += per * src_head;
+      if (i + 1 < to) load();
+      if (kind < 2 && gain) {
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(a[j], a[j], fmaf(b[j], b[j], ss));
+        for (int j = 0; j < 8; ++j) {
+          s0 = fmaf(a[j], a[j], s0);
+          s1 = fmaf(b[j], b[j], s1);
+        }
+        float ss = s0 + s1;
         for (int o = lanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float inv = 1.0f / sqrtf(ss / (float)p.D + p.eps);
 #pragma unroll
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const RopeParams p, i
           b[j] = b[j] * inv * gb[j];
         }
       }
-      if (turns) {
+      if (kind < 2 && turns) {
         if constexpr (INTER) {
           // pairs past rotary_dim keep their values (not 1 x + 0 y: y may be infinite)
 #pragma unroll
@@ -204,26 +209,32 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const RopeParams p, i
           }
         }
       }
-    }
-    if (!ok) continue;
-    if (is_q || (!is_v && p.k_out)) {
-      T *dst = is_q ? static_cast<T *>(p.q_out) + (long long)t * p.qo_tok + (long long)h * p.qo_head
-                    : static_cast<T *>(p.k_out) + (long long)t * p.ko_tok + (long long)h * p.ko_head;
-      *reinterpret_cast<uint4 *>(dst + ea) = pack8<T>(a);
-      *reinterpret_cast<uint4 *>(dst + eb) = pack8<T>(b);
-    }
-    if (!is_q && slot >= 0) {
-      char *dst = (is_v ? p.cv : p.ck) + row + (long long)h * p.head_b;
-      if constexpr (F8) {
-        const float scale = is_v ? p.v_scale : p.k_scale;
-        *reinterpret_cast<uint2 *>(dst + ea) = pack8_e4m3(a, scale);
-        *reinterpret_cast<uint2 *>(dst + eb) = pack8_e4m3(b, scale);
-      } else {
-        *reinterpret_cast<uint4 *>(dst + 2 * ea) = pack8<T>(a);
-        *reinterpret_cast<uint4 *>(dst + 2 * eb) = pack8<T>(b);
+      if (ok) {
+        if (kind == 0 || (kind == 1 && p.k_out)) {
+          *reinterpret_cast<uint4 *>(out + ea) = pack8<T>(a);
+          *reinterpret_cast<uint4 *>(out + eb) = pack8<T>(b);
+        }
+        if (kind > 0 && row >= 0) {
+          if constexpr (F8) {
+            *reinterpret_cast<uint2 *>(cache + ea) = pack8_e4m3(a, scale);
+            *reinterpret_cast<uint2 *>(cache + eb) = pack8_e4m3(b, scale);
+          } else {
+            *reinterpret_cast<uint4 *>(cache + 2 * ea) = pack8<T>(a);
+            *reinterpret_cast<uint4 *>(cache + 2 * eb) = pack8<T>(b);
+          }
+        }
       }
+      out += per * out_head;
+      cache += per * p.head_b;
     }
-  }
+  };
+  const long long tt = t, at = row < 0 ? 0 : row;
+  heads_of(std::integral_constant<int, 0>{}, i0, min(i1, pq), static_cast<const T *>(p.q) + tt * p.q_tok, p.q_head, p.nq,
+           p.q_gain, static_cast<T *>(p.q_out) + tt * p.qo_tok, p.qo_head, p.ck, 1.f);
+  heads_of(std::integral_constant<int, 1>{}, max(i0 - pq, 0), min(i1 - pq, pk), static_cast<const T *>(p.k) + tt * p.k_tok,
+           p.k_head, p.nkv, p.k_gain, static_cast<T *>(p.k_out) + tt * p.ko_tok, p.ko_head, p.ck + at, p.k_scale);
+  heads_of(std::integral_constant<int, 2>{}, max(i0 - pq - pk, 0), i1 - pq - pk, static_cast<const T *>(p.v) + tt * p.v_tok,
+           p.v_head, p.nkv, nullptr, static_cast<T *>(nullptr), 0, p.cv + at, p.v_scale);
 }
 
 template <typename T> int launch_rope(const RopeParams &p, bool inter, bool f8, int num_sms, cudaStream_t s) {

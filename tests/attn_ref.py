@@ -21,7 +21,7 @@ def cache_rows(cache, layer, kind, page, off):
     t = t if t.dim() == 4 else t[layer]
     raw = t.view(torch.uint8)
     got = raw[page, off] if cache.layout == "NHD" else raw[page, :, off]
-    scale = cache.struct.k_scale if kind == "k" else cache.struct.v_scale
+    scale = cache.k_scale if kind == "k" else cache.v_scale
     return values(got.contiguous().view(t.dtype)) * scale
 
 

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import mixture_experts_gemv_b200 as moe
-from mixture_experts_gemv_b200._lib import _HeadsStruct, _KvCacheStruct
+from mixture_experts_gemv_b200._lib import _HEADS, _KV_CACHE
 
 FAKE = 1 << 20   # an aligned address that nothing here follows
 
@@ -23,11 +23,12 @@ def kv(**change):
     a = dict(k=FAKE, v=FAKE + (1 << 30), dtype=moe.MOE_DT_BF16, n_layers=2, num_pages=50, page_size=16, n_kv=2, head_dim=64,
              layer_stride=50 * 2048, page_stride=2048, token_stride=128, head_stride=64, k_scale=1.0, v_scale=1.0)
     a.update(change)
-    return ctypes.byref(_KvCacheStruct(*[a[n] for n, _ in _KvCacheStruct._fields_]))
+    a["k"] = a["k"] or 0
+    return _KV_CACHE.pack(*a.values())
 
 
 def heads(at=FAKE, token=512, head=64):
-    return ctypes.byref(_HeadsStruct(at, token, head))
+    return _HEADS.pack(at or 0, token, head)
 
 
 def code(L, rc, want, text=""):
@@ -162,13 +163,12 @@ def test_binding_refuses_what_the_library_cannot_see():
 
 def test_one_cache_descriptor_for_both_orders_and_layers():
     nhd = torch.zeros(3, 7, 16, 2, 64, dtype=torch.float8_e4m3fn)
-    a = moe.MoeKvCache(nhd, nhd.clone(), "NHD", 0.5, 0.25).struct
-    assert (a.n_layers, a.num_pages, a.page_size, a.n_kv, a.head_dim, a.dtype) == (3, 7, 16, 2, 64, moe.MOE_DT_E4M3)
-    assert (a.layer_stride, a.page_stride, a.token_stride, a.head_stride) == (7 * 2048, 2048, 128, 64)
+    a = moe.MoeKvCache(nhd, nhd.clone(), "NHD", 0.5, 0.25)
+    assert _KV_CACHE.unpack(a.packed)[2:] == (moe.MOE_DT_E4M3, 3, 7, 16, 2, 64, 7 * 2048, 2048, 128, 64, 0.5, 0.25)
     hnd = torch.zeros(7, 2, 16, 64, dtype=torch.float16)
-    b = moe.MoeKvCache(hnd, hnd.clone(), "HND").struct
-    assert (b.n_layers, b.num_pages, b.page_size, b.n_kv, b.dtype) == (1, 7, 16, 2, moe.MOE_DT_F16)
-    assert (b.page_stride, b.token_stride, b.head_stride) == (2048, 64, 1024)
+    b = moe.MoeKvCache(hnd, hnd.clone(), "HND")
+    assert _KV_CACHE.unpack(b.packed)[2:] == (moe.MOE_DT_F16, 1, 7, 16, 2, 64, 0, 2048, 64, 1024, 1.0, 1.0)
+    assert (b.n_layers, b.num_pages, b.page_size, b.n_kv, b.head_dim) == (1, 7, 16, 2, 64)
 
 
 def test_frequencies():

@@ -390,7 +390,7 @@ def test_norm_rope_and_append(T, nq, nkv, D, rot, inter, norm, far, dtype, cache
     assert ((q_out.double() - yq).abs() <= ref.rotated_bound(yq, size, D, dtype)).all()
     yk, size = ref.rotated(k, kg, 1e-6, pos, inv, inter, 1.25)
     assert ((k_out.double() - yk).abs() <= ref.rotated_bound(yk, size, D, dtype)).all()
-    ks, vs = cache.struct.k_scale, cache.struct.v_scale
+    ks, vs = cache.k_scale, cache.v_scale
     ok = slots >= 0
     at = slots[ok]
     got = ref.cache_rows(cache, 0, "k", at // page, at % page)
