@@ -33,7 +33,7 @@ struct AttnParams {
   int max_tokens;                        // that a block table can hold
   const int32_t *lens;
   int B, nq, nkv, D, group, n_groups;    // group = nq / nkv; n_groups: CTA passes over a KV head's group
-  int page_size, num_pages, window;
+  int page_size, page_shift, num_pages, window;   // page_shift: log2 of a power of two, else -1
   int groups_of_8;                       // 8 tokens from a multiple of 8 on always lie in one page
   float scale_log2;                      // scale * log2(e) * k_scale
   float v_scale;
@@ -42,8 +42,6 @@ struct AttnParams {
   float *lse;                            // [B, nq] or null
   float *ws_o;                           // [2 workers][D / 16][column tiles][32 lanes][4] unnormalised sums
   float2 *ws_ml;                         // [2 workers][rows] maximum (log2) and sum
-  int4 *rec;                             // (first worker + 1 or 0, sequence, segment, last worker) of cut segments
-  int rec_by_segment;                    // one record a segment, else one a worker
   uint32_t *err;
 };
 

@@ -285,7 +285,7 @@ int moe_rope_frequencies(int kind, int rotary_dim, double base, double factor, d
   return MOE_OK;
 }
 
-// Layout of the workspace: partial sums, then (maximum, sum) pairs, then the records of cut segments.
+// Layout of the workspace: partial sums, then (maximum, sum) pairs.
 static size_t attn_rows(int n_q, int n_kv, int D) { return 8 * (size_t)moe_attn_tiles(D, n_q / n_kv); }
 static size_t attn_o_bytes(size_t rows, int D) { return 2ull * MOE_ATTN_MAX_WORKERS * rows * D * 4; }
 static size_t attn_ml_bytes(size_t rows) { return 2ull * MOE_ATTN_MAX_WORKERS * rows * 8; }
@@ -293,7 +293,7 @@ static size_t attn_ml_bytes(size_t rows) { return 2ull * MOE_ATTN_MAX_WORKERS * 
 size_t moe_attention_decode_workspace_bytes(int n_q, int n_kv, int head_dim) {
   if (n_q < 1 || n_kv < 1 || n_q % n_kv || head_dim < 16 || head_dim > 512 || head_dim % 16) return 0;
   const size_t rows = attn_rows(n_q, n_kv, head_dim);
-  return attn_o_bytes(rows, head_dim) + attn_ml_bytes(rows) + MOE_ATTN_MAX_WORKERS * sizeof(int4);
+  return attn_o_bytes(rows, head_dim) + attn_ml_bytes(rows);
 }
 
 int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cache, int layer, const int32_t *block_tables,
@@ -347,6 +347,7 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
   p.group = n_q / cache->n_kv;
   p.n_groups = (p.group + (int)rows - 1) / (int)rows;
   p.page_size = cache->page_size;
+  p.page_shift = (cache->page_size & (cache->page_size - 1)) ? -1 : __builtin_ctz(cache->page_size);
   p.num_pages = cache->num_pages;
   p.window = window;
   p.groups_of_8 = cache->page_size % 8 == 0 && p.tok_b < (1ll << 28);   // row offsets within a group in 32 bits
@@ -357,7 +358,6 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
   char *ws = static_cast<char *>(workspace);
   p.ws_o = reinterpret_cast<float *>(ws);
   p.ws_ml = reinterpret_cast<float2 *>(ws + attn_o_bytes(rows, D));
-  p.rec = reinterpret_cast<int4 *>(ws + attn_o_bytes(rows, D) + attn_ml_bytes(rows));
   p.err = dev->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   rc = cache->dtype == MOE_DT_E4M3 ? moe_launch_attn_e4m3(p, dev->num_sms, dtype == MOE_DT_BF16, s)

@@ -105,7 +105,7 @@ template <int W, int NT, int ES> struct Shape {
   // 16-token row tiles a warp takes per step: two where a row is short, which halves the share
   // of the softmax's shuffles and of the loop (not with 32 heads and more: registers)
   static constexpr int kTiles = kRow <= 256 && NT <= 2 ? 2 : 1;
-  static constexpr int kTok = 16 * kTiles;          // tokens of a unit
+  static constexpr int kTok = 16 * kTiles, kLog = kTiles == 1 ? 4 : 5;   // tokens of a unit, and log2
   static constexpr int kUnit = kTok * kRow;         // bytes of its K or V rows
   // Slots of kUnit in a warp's ring: 96 KB a CTA, two CTAs an SM (192 KB and one where a slot is
   // 16 KB): at least 128 KB of copies in flight on an SM
@@ -120,23 +120,21 @@ template <int W, int NT, int ES> struct Shape {
   static __device__ __forceinline__ constexpr uint32_t at(uint32_t base, int k) { return (base ^ (uint32_t)((k & 3) << 5)) + (k >> 2) * 128; }
 };
 
-// Keys [lo, len) of a sequence: n units from unit number lo / TOK on. A bad length is cut to what
-// the table can hold.
+// Keys [lo, len) of a sequence: n units of 2^LOG tokens from unit number lo >> LOG on. A bad length is
+// cut to what the table can hold.
 struct Span {
   int len, lo, n;
-};
-template <int TOK> __device__ __forceinline__ Span span_of(const AttnParams &p, int b) {
-  Span s;
-  int len = p.lens[b];
-  if ((unsigned)len > (unsigned)p.max_tokens) {
-    atomicCAS(p.err, 0u, MOE_DEV_ERR_BAD_LENGTH);
-    len = len < 0 ? 0 : p.max_tokens;
+  __device__ __forceinline__ Span() : len(0), lo(0), n(0) {}
+  __device__ __forceinline__ Span(const AttnParams &p, int length, int log) {
+    if ((unsigned)length > (unsigned)p.max_tokens) {
+      atomicCAS(p.err, 0u, MOE_DEV_ERR_BAD_LENGTH);
+      length = length < 0 ? 0 : p.max_tokens;
+    }
+    len = length;
+    lo = p.window > 0 && len > p.window ? len - p.window : 0;
+    n = len > 0 ? ((len - 1) >> log) + 1 - (lo >> log) : 0;
   }
-  s.len = len;
-  s.lo = p.window > 0 && len > p.window ? len - p.window : 0;
-  s.n = len > 0 ? (len - 1) / TOK + 1 - s.lo / TOK : 0;
-  return s;
-}
+};
 
 static __device__ __noinline__ long long quotient64(long long a, int b) { return a / b; }
 __device__ __forceinline__ long long quotient(long long a, int b) {   // a >= 0; 32-bit division where it fits
@@ -148,6 +146,7 @@ __device__ __forceinline__ long long quotient(long long a, int b) {   // a >= 0;
 struct Split {
   int workers, longer;
   long long each;
+  Split() = default;
   __device__ __forceinline__ Split(long long total, int most) {
     workers = total < most ? (int)total : most;
     each = workers ? quotient(total, workers) : 0;
@@ -202,8 +201,103 @@ struct Joined {
   }
 };
 
-// A place in the numbering of units: unit i of n of segment seg of sequence b.
-template <int TOK> struct Cursor {
+// The numbering of the call's work. A segment (sequence, KV head, head group) costs its units and,
+// where workers have several, one more that comes first: its q, its ends and its result (eight
+// one-unit segments in one warp's range took 5 to 8 us beside a 36 us stream of 40,000 tokens).
+// Every worker's range of costs still holds a unit: no two of the extra ones are neighbours.
+// Held by a warp: lane l has sequence base + l of the strip of 32 that was looked at last.
+struct Numbering {
+  static constexpr unsigned kAll = 0xffffffffu;
+  int segs, extra, log;
+  long long units;      // of all sequences, for one segment each
+  Split split;
+  int base;             // the strip, and what comes before it
+  long long before;     // units
+  int before_filled;    // sequences with a key
+  int n, filled;        // the lane's units, and sequences with a key up to it
+  long long inc;        // units up to the lane's sequence, inclusive
+  int len;              // the lane's length
+
+  __device__ __forceinline__ void strip(const AttnParams &p, int at) {
+    const int lane = threadIdx.x & 31;
+    base = at;
+    len = base + lane < p.B ? __ldcg(p.lens + base + lane) : 0;
+    n = Span(p, len, log).n;
+    unsigned sum = n;   // of 32 lengths below 2^30 over 16: fits
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned t = __shfl_up_sync(kAll, sum, o);
+      if (lane >= o) sum += t;
+    }
+    inc = before + sum;
+    filled = before_filled + __popc(__ballot_sync(kAll, n > 0) & (kAll >> (31 - lane)));
+  }
+  __device__ __forceinline__ void next_strip(const AttnParams &p) {
+    before = __shfl_sync(kAll, inc, 31);
+    before_filled = __shfl_sync(kAll, filled, 31);
+    strip(p, base + 32);
+  }
+  __device__ __forceinline__ Numbering(const AttnParams &p, int log_, int all_workers) : segs(p.nkv * p.n_groups), extra(0), log(log_), before(0), before_filled(0) {
+    strip(p, 0);
+    units = __shfl_sync(kAll, inc, 31);
+    int with_key = __shfl_sync(kAll, filled, 31);
+    if (p.B > 32) {
+      long long more = 0;
+      int more_keys = 0;
+#pragma unroll 1
+      for (int b = 32 + (threadIdx.x & 31); b < p.B; b += 32) {
+        const int m = Span(p, __ldcg(p.lens + b), log).n;
+        more += m;
+        more_keys += m > 0;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        more += __shfl_xor_sync(kAll, more, o);
+        more_keys += __shfl_xor_sync(kAll, more_keys, o);
+      }
+      units += more;
+      with_key += more_keys;
+    }
+    extra = (units + with_key) * segs >= 2ll * all_workers ? 1 : 0;
+    split = Split((units + extra * with_key) * segs, all_workers);
+  }
+  // A segment: its sequence, number there, units and first cost.
+  struct Segment {
+    int b, seg, n, len;
+    long long first;
+    long long units_before;   // units of all segments before it
+  };
+  __device__ __forceinline__ Segment segment(int src, int seg) const {   // of the strip's sequence src
+    Segment s;
+    s.b = base + src;
+    s.seg = seg;
+    s.n = __shfl_sync(kAll, n, src);
+    s.len = __shfl_sync(kAll, len, src);
+    const long long u = __shfl_sync(kAll, inc, src) - s.n;
+    const int f = __shfl_sync(kAll, filled, src) - 1;
+    s.first = (u + extra * f) * segs + (long long)seg * (s.n + extra);
+    s.units_before = u * segs + (long long)seg * s.n;
+    return s;
+  }
+  // The segment that holds a cost below the total, not before the last one asked for.
+  __device__ __forceinline__ Segment holding(const AttnParams &p, long long cost) {
+    unsigned hit;
+#pragma unroll 1
+    while (!(hit = __ballot_sync(kAll, cost < (inc + extra * filled) * segs))) next_strip(p);
+    const int src = __ffs(hit) - 1;
+    Segment s = segment(src, 0);
+    s.seg = (int)quotient(cost - s.first, s.n + extra);
+    s.first += (long long)s.seg * (s.n + extra);
+    s.units_before += (long long)s.seg * s.n;
+    return s;
+  }
+  __device__ __forceinline__ int unit(const Segment &s, long long cost) const { return max((int)(cost - s.first) - extra, 0); }
+  __device__ __forceinline__ int first_worker(long long first) const { return split.owner(first + extra); }
+  __device__ __forceinline__ int last_worker(long long first, int n_) const { return split.owner(first + extra + n_ - 1); }
+};
+
+// A place in the numbering: unit i of segment seg of sequence b.
+template <int LOG> struct Cursor {
   int b, seg, i;
   Span sp;
   __device__ __forceinline__ void next(const AttnParams &p, int segs) {   // not past the last unit
@@ -212,11 +306,12 @@ template <int TOK> struct Cursor {
     if (++seg < segs) return;
     seg = 0;
 #pragma unroll 1
-    do sp = span_of<TOK>(p, ++b);
+    do sp = Span(p, __ldg(p.lens + ++b), LOG);
     while (sp.n == 0);
   }
-  __device__ __forceinline__ int token() const { return (sp.lo / TOK + i) * TOK; }   // the unit's first
+  __device__ __forceinline__ int token() const { return ((sp.lo >> LOG) + i) << LOG; }   // the unit's first
 };
+__device__ __forceinline__ int kv_head(const AttnParams &p, int seg) { return p.n_groups == 1 ? seg : seg / p.n_groups; }
 
 // One accumulator fragment (two heads' values at two elements, x inv) into the rows of a KV head's
 // group: out points at head 8 n, `heads` of them exist. 16 ES-dependent elements from 16 k on.
@@ -256,38 +351,16 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
   pdl_launch_dependents();
 
   // ---- the warp's range of units
-  const int segs = p.nkv * p.n_groups;
   const int all_workers = kWarps * gridDim.x;
-  const int n_first = lane < p.B ? span_of<S::kTok>(p, lane).n : 0;   // of the first 32 sequences
-  long long units = n_first;
-  int filled = n_first > 0;   // sequences with a key
-#pragma unroll 1
-  for (int b = 32 + lane; b < p.B; b += 32) {
-    const int n = span_of<S::kTok>(p, b).n;
-    units += n;
-    filled += n > 0;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    units += __shfl_xor_sync(kAll, units, o);
-    filled += __shfl_xor_sync(kAll, filled, o);
-  }
-  // A segment costs its units and, where workers have several, one more: its q, its ends and its
-  // result (eight one-unit segments in one warp's range took 5 to 8 us beside a 36 us stream of
-  // 40,000 tokens). Every worker's range still holds a unit: no two of these are neighbours.
-  const int extra = (units + filled) * segs >= 2ll * all_workers ? 1 : 0;
-  const Split split((units + extra * filled) * segs, all_workers);
-  const int workers = split.workers;
+  Numbering num(p, S::kLog, all_workers);
+  const int segs = num.segs, workers = num.split.workers;
   // Neighbours in the numbering are on different SMs where there is little to do, else in one
   // block, which can then join its warps' pieces
-  const int worker = extra ? blockIdx.x * kWarps + warp : warp * gridDim.x + blockIdx.x;
+  const int worker = num.extra ? blockIdx.x * kWarps + warp : warp * gridDim.x + blockIdx.x;
   // sequences without a key: rows of zeros, lse = -inf
 #pragma unroll 1
   for (int b = worker; b < p.B; b += all_workers) {
-    if (span_of<S::kTok>(p, b).n) continue;
-    if (p.rec_by_segment)
-#pragma unroll 1
-      for (int i = lane; i < segs; i += 32) p.rec[b * segs + i] = make_int4(0, 0, 0, 0);
+    if (Span(p, __ldg(p.lens + b), S::kLog).n) continue;
 #pragma unroll 1
     for (int h = 0; h < p.nq; ++h) {
 #pragma unroll 1
@@ -295,59 +368,32 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
       if (p.lse && lane == 0) p.lse[(long long)b * p.nq + h] = ninf;
     }
   }
-  if (worker >= workers) {
-    if (!p.rec_by_segment && lane == 0) p.rec[worker] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  // Numbering of costs: a segment's extra one, then its units. The units at costs [from, to):
-  const long long from = split.first(worker), to = split.first(worker + 1);
-  Cursor<S::kTok> at;        // the unit that is computed next
-  long long seg_first = 0;   // cost number of its segment's start
-  int count = 0;             // the warp's units
+  if (worker >= workers) return;
+  Cursor<S::kLog> at;        // the unit that is computed next
+  long long seg_first;       // first cost of its segment
+  int count;                 // the warp's units
   {
-    long long before = 0, units_before = 0;   // costs and units of the earlier sequences
-    long long begin = -1;                     // units before `from`
-#pragma unroll 1
-    for (int base = 0;; base += 32) {
-      const int b = base + lane;
-      const long long n = base ? (b < p.B ? span_of<S::kTok>(p, b).n : 0) : n_first;
-      long long inc = n ? (n + extra) * segs : 0, inc_units = n * segs;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(kAll, inc, o), tu = __shfl_up_sync(kAll, inc_units, o);
-        if (lane >= o) inc += t, inc_units += tu;
-      }
-#pragma unroll 1
-      for (int end = 0; end < 2; ++end) {   // first `from`, then `to`: a cost's sequence, segment and unit
-        if ((end == 0) != (begin < 0)) continue;
-        const unsigned hit = __ballot_sync(kAll, end == 0 ? from < before + inc : to <= before + inc);
-        if (!hit) break;
-        const int src = __ffs(hit) - 1, sn = (int)__shfl_sync(kAll, n, src);
-        const long long first = before + __shfl_sync(kAll, inc, src) - (long long)(sn + extra) * segs;
-        const long long rel = (end == 0 ? from : to) - first;
-        const int seg = (int)quotient(rel, sn + extra);
-        const int i = max((int)(rel - (long long)seg * (sn + extra)) - extra, 0);
-        const long long mine = units_before + __shfl_sync(kAll, inc_units, src) - (long long)sn * segs + (long long)seg * sn + i;
-        if (end == 0) {
-          at.b = base + src;
-          at.seg = seg;
-          at.i = i;
-          seg_first = first + (long long)seg * (sn + extra);
-          begin = mine;
-        } else {
-          count = (int)(mine - begin);
-        }
-      }
-      if (count) break;
-      before += __shfl_sync(kAll, inc, 31);
-      units_before += __shfl_sync(kAll, inc_units, 31);
+    const long long from = num.split.first(worker), to = num.split.first(worker + 1);
+    const Numbering::Segment s = num.holding(p, from);
+    at.b = s.b;
+    at.seg = s.seg;
+    at.i = num.unit(s, from);
+    at.sp = Span(p, s.len, S::kLog);
+    seg_first = s.first;
+    const long long begin = s.units_before + at.i;
+    if (worker + 1 == workers) {
+      count = (int)(num.units * segs - begin);
+    } else {
+      const Numbering::Segment e = num.holding(p, to);
+      count = (int)(e.units_before + num.unit(e, to) - begin);
     }
-    at.sp = span_of<S::kTok>(p, at.b);
   }
+  const Split split = num.split;
+  const int extra = num.extra;
 
   // ---- loader: runs ahead of the computation by the ring's slots, and its look-ups in the block
   // tables by two units more
-  Cursor<S::kTok> ahead = at;   // the unit that is looked up next
+  Cursor<S::kLog> ahead = at;   // the unit that is looked up next
   int to_look_up = count, to_copy = count;
   struct Found {                // a looked-up unit, as lane r holds it for token r
     int page, in_page, kvh, first, last;   // tokens [first, last) of the unit are keys
@@ -357,12 +403,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
     const int t0 = ahead.token(), t = t0 + (lane & (S::kTok - 1));
     f.first = max(ahead.sp.lo - t0, 0);
     f.last = min(ahead.sp.len - t0, S::kTok);
-    f.kvh = ahead.seg / p.n_groups;
-    f.page = 0;
+    f.kvh = kv_head(p, ahead.seg);
     // with pages of whole 8-token groups, every lane of a group that holds a key has the group's page
     const int lo = p.groups_of_8 ? ahead.sp.lo & ~7 : ahead.sp.lo, hi = p.groups_of_8 ? (ahead.sp.len + 7) & ~7 : ahead.sp.len;
     if (t >= lo && t < hi) {
-      const unsigned e = (unsigned)t / (unsigned)p.page_size;
+      const unsigned e = p.page_shift >= 0 ? (unsigned)t >> p.page_shift : (unsigned)t / (unsigned)p.page_size;
       f.in_page = t - (int)e * p.page_size;
       f.page = __ldg(p.tables + (long long)ahead.b * p.table_stride + e);
     } else {
@@ -371,7 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
     if (--to_look_up > 0) {
       ahead.next(p, segs);
       if (ahead.i == 0) {   // a new segment: its q rows on their way to L1 (a lane per 128 bytes)
-        const int kvh = ahead.seg / p.n_groups, h0 = kvh * p.group + (ahead.seg - kvh * p.n_groups) * S::kRows;
+        const int kvh = kv_head(p, ahead.seg), h0 = kvh * p.group + (ahead.seg - kvh * p.n_groups) * S::kRows;
         const int lines = (p.D * 2 + 127) / 128, heads = min(S::kRows, (kvh + 1) * p.group - h0);
 #pragma unroll 1
         for (int i = lane; i < heads * lines; i += 32) {
@@ -464,12 +509,15 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
   then = now;
   look_up(then);
 
-  int4 rec = make_int4(0, 0, 0, 0);
   int slot = 0, done = 0, lead = S::kSlots - 1;   // lead: copies issued before the first is waited for
   while (true) {   // a piece: the units of one segment that are the warp's
-    const int kvh = at.seg / p.n_groups, h0 = kvh * p.group + (at.seg - kvh * p.n_groups) * S::kRows;
+    const int kvh = kv_head(p, at.seg), h0 = kvh * p.group + (at.seg - kvh * p.n_groups) * S::kRows;
     const int heads = min(S::kRows, (kvh + 1) * p.group - h0);
     const int i0 = at.i, cnt = min(at.sp.n - i0, count - done);
+    const bool whole = cnt == at.sp.n;
+    // whether the block's four warps have nothing but parts of this segment
+    const bool in_block = !whole && extra &&
+                          Block(blockIdx.x).inside(split.owner(seg_first + extra), split.owner(seg_first + extra + at.sp.n - 1));
 
     uint32_t qf[W / 16][NT][2];
     float sc[NT][2];   // score scale of the lane's two columns
@@ -719,25 +767,22 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
 
     // ---- the piece's result
     done += cnt;
-    const bool whole = cnt == at.sp.n;
-    float inv[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(kAll, l[n][e], x);
-        inv[n][e] = l[n][e] == 0.f ? 0.f : p.v_scale / l[n][e];
-      }
     if (whole) {
       TO *out = static_cast<TO *>(p.out) + (long long)at.b * p.out_tok + (long long)h0 * p.out_head;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        const float inv0 = l[n][0] == 0.f ? 0.f : p.v_scale / l[n][0], inv1 = l[n][1] == 0.f ? 0.f : p.v_scale / l[n][1];
 #pragma unroll
         for (int k = 0; k < W / 16; ++k)
           if (16 * k < p.D)
             store_fragment<TO, ES>(out + 8 * n * p.out_head, p.out_head, k, heads - 8 * n, lane,
-                                   make_float4(o[k][n][0], o[k][n][1], o[k][n][2], o[k][n][3]), inv[n][0], inv[n][1]);
+                                   make_float4(o[k][n][0], o[k][n][1], o[k][n][2], o[k][n][3]), inv0, inv1);
         if (p.lse && g == 0) {
           float *lse = p.lse + (long long)at.b * p.nq + h0 + 8 * n + 2 * c;
           if (8 * n + 2 * c < heads) lse[0] = (mx[n][0] + (log2f(l[n][0]) - M::kOff)) * kLn2;
@@ -745,10 +790,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
         }
       }
     } else {
-      const int w0 = split.owner(seg_first + extra), w1 = split.owner(seg_first + extra + at.sp.n - 1);
       float4 *ws = reinterpret_cast<float4 *>(p.ws_o), *ws_ml = reinterpret_cast<float4 *>(p.ws_ml);
-      if (extra && Block(blockIdx.x).inside(w0, w1)) {
-        // the block's four warps have nothing but parts of this segment: one piece of them
+      if (in_block) {   // one piece of the four
         __shared__ float4 sh_ml[kWarps][4 * NT];
         float4 *mine = reinterpret_cast<float4 *>(smem + warp * (S::kSlots * S::kUnit)) + lane;
         __syncwarp();
@@ -786,38 +829,60 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
           for (int n = 0; n < NT; ++n) ws_ml[piece * (4 * NT) + 4 * n + c] = make_float4(mx[n][0], l[n][0], mx[n][1], l[n][1]);
         }
       }
-      if (i0 == 0) rec = make_int4(worker + 1, at.b, at.seg, w1 | (extra << 30));
     }
-    if (i0 == 0 && p.rec_by_segment && lane == 0) p.rec[at.b * segs + at.seg] = whole ? make_int4(0, 0, 0, 0) : rec;
     if (done == count) break;
     seg_first += at.sp.n + extra;
     at.i = at.sp.n - 1;
     at.next(p, segs);
   }
-  if (!p.rec_by_segment && lane == 0) p.rec[worker] = rec;
 }
 
-// Sums the pieces of record blockIdx.x's segment. A thread takes one fragment of a piece (two heads
-// at two elements: four values), of every par-th piece (the block's threads are par groups over the
-// same threads / par fragments), and joins them as it goes, so that only the record is waited for
-// before the pieces' loads; then the groups are joined pairwise through shared memory.
+// Sums the pieces of one cut segment: segment blockIdx.x (by_segment), or the one that starts in
+// worker blockIdx.x and goes on behind it. Which workers have its pieces follows from the lengths,
+// before the attention kernel's results are waited for (that kernel lets this one start only when
+// what came before it is done, so the lengths are there). A thread takes one fragment of a piece
+// (two heads at two elements: four values), of every par-th piece: the block's threads are par
+// groups over the same threads / par fragments. Then the groups' sums are joined.
 constexpr int kJoinMost = 512;   // threads
+constexpr int kJoinPar = 16;     // groups
 template <typename TO, int ES>
-__global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int nt, int par, float off) {
-  __shared__ float4 s_acc[kJoinMost / 2], s_ml[kJoinMost / 2];
-  pdl_wait();
-  const int4 rec = p.rec[blockIdx.x];
-  if (!rec.x) return;
+__global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int log, int all_workers, int by_segment, int nt, int par, float off) {
+  __shared__ float4 s_acc[kJoinMost], s_ml[kJoinMost];
+  int w0, w1, b, seg;
+  bool joined;
+  {
+    Numbering num(p, log, all_workers);
+    joined = num.extra;
+    Numbering::Segment s;
+    if (by_segment) {
+      const int seq = blockIdx.x / num.segs;
+#pragma unroll 1
+      while (seq >= num.base + 32) num.next_strip(p);
+      s = num.segment(seq - num.base, blockIdx.x - seq * num.segs);
+      if (s.n == 0) return;
+      w0 = num.first_worker(s.first);
+    } else {
+      w0 = blockIdx.x;
+      if (w0 + 1 >= num.split.workers) return;
+      s = num.holding(p, num.split.first(w0 + 1) - 1);
+      if (num.first_worker(s.first) != w0) return;
+    }
+    w1 = num.last_worker(s.first, s.n);
+    if (w1 == w0) return;
+    b = s.b;
+    seg = s.seg;
+  }
   const int tid = threadIdx.x, lane = tid & 31, per = blockDim.x / par, j0 = tid / per;   // per: a multiple of 32
   const int frags = p.D / 16 * nt * 32, f = blockIdx.y * per + (tid - j0 * per);
   const int k = f / (32 * nt), n = f / 32 - k * nt, c = lane & 3;
-  const int b = rec.y, kvh = rec.z / p.n_groups, h0 = kvh * p.group + (rec.z - kvh * p.n_groups) * 8 * nt + 8 * n;
+  const int kvh = kv_head(p, seg), h0 = kvh * p.group + (seg - kvh * p.n_groups) * 8 * nt + 8 * n;
   const int heads = (kvh + 1) * p.group - h0;   // that exist from this column tile on
-  const Pieces pieces(rec.x - 1, rec.w & 0x3fffffff, rec.w >> 30);
+  const Pieces pieces(w0, w1, joined);
+  const float4 *po = reinterpret_cast<const float4 *>(p.ws_o) + f, *pm = reinterpret_cast<const float4 *>(p.ws_ml) + (4 * n + c);
+  pdl_wait();
   Joined sum;
   if (f < frags) {
     constexpr int kAhead = 4;
-    const float4 *po = reinterpret_cast<const float4 *>(p.ws_o) + f, *pm = reinterpret_cast<const float4 *>(p.ws_ml) + (4 * n + c);
     for (int j = j0; j < pieces.count; j += kAhead * par) {
       float4 m[kAhead], v[kAhead];
 #pragma unroll
@@ -834,16 +899,33 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
         if (j + x * par < pieces.count) sum.take(m[x], v[x]);
     }
   }
-  for (int half = par >> 1; half; half >>= 1) {
+  if (par > 1) {
+    s_acc[tid] = sum.acc;
+    s_ml[tid] = sum.ml;
     __syncthreads();
-    if (j0 >= half && j0 < 2 * half) {
-      s_acc[tid - half * per] = sum.acc;
-      s_ml[tid - half * per] = sum.ml;
+    if (j0) return;
+    // the maximum first, so that the groups' exponentials do not wait for one another
+    const float ninf = __int_as_float(0xff800000);
+    float m0 = sum.ml.x, m1 = sum.ml.z;
+    for (int j = 1; j < par; ++j) {
+      m0 = fmaxf(m0, s_ml[j * per + tid].x);
+      m1 = fmaxf(m1, s_ml[j * per + tid].z);
     }
-    __syncthreads();
-    if (j0 < half) sum.take(s_ml[tid], s_acc[tid]);
+    const float b0 = m0 == ninf ? 0.f : m0, b1 = m1 == ninf ? 0.f : m1;
+    float l0 = 0.f, l1 = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = 0; j < par; ++j) {
+      const float4 ml = s_ml[j * per + tid], v = s_acc[j * per + tid];
+      const float f0 = exp2_fast(ml.x - b0), f1 = exp2_fast(ml.z - b1);
+      l0 = fmaf(f0, ml.y, l0);
+      l1 = fmaf(f1, ml.w, l1);
+      a = make_float4(fmaf(f0, v.x, a.x), fmaf(f1, v.y, a.y), fmaf(f0, v.z, a.z), fmaf(f1, v.w, a.w));
+    }
+    sum.ml = make_float4(m0, l0, m1, l1);
+    sum.acc = a;
   }
-  if (j0 || f - lane >= frags) return;   // whole warps
+  if (f - lane >= frags) return;   // whole warps
   TO *out = static_cast<TO *>(p.out) + (long long)b * p.out_tok + (long long)h0 * p.out_head;
   store_fragment<TO, ES>(out, p.out_head, k, heads, lane, sum.acc, sum.ml.y == 0.f ? 0.f : p.v_scale / sum.ml.y,
                            sum.ml.w == 0.f ? 0.f : p.v_scale / sum.ml.w);
@@ -868,12 +950,8 @@ template <typename T, int W, int NT, int ES, bool QB> int launch(const AttnParam
   }
   int grid = num_sms * occ;
   if (grid * kWarps > MOE_ATTN_MAX_WORKERS) grid = MOE_ATTN_MAX_WORKERS / kWarps;
-  AttnParams a = p;
-  // A record a segment where there are fewer segments than workers, else a record a worker: the
-  // join's grid is as small as can be said without the lengths
   const long long segments = (long long)p.B * p.nkv * p.n_groups;
   const int workers = grid * kWarps;
-  a.rec_by_segment = segments <= workers;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -884,17 +962,19 @@ template <typename T, int W, int NT, int ES, bool QB> int launch(const AttnParam
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, a) != cudaSuccess) return -1;
+  if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) return -1;
   // Threads that share a fragment in the join: as many as a quarter of the pieces that a segment
   // has when all are equally long and blocks join theirs, so that each one's loads are in flight
   // together
   int par = 1;
-  while (par < 16 && 4 * par * segments < grid) par *= 2;
+  while (par < kJoinPar && 4 * par * segments < grid) par *= 2;
   const int threads = par > 4 ? kJoinMost : kJoinMost / 2, frags = p.D / 16 * NT * 32, per = threads / par;
-  cfg.gridDim = dim3(a.rec_by_segment ? (unsigned)segments : workers, (frags + per - 1) / per);
+  // a block a segment where there are fewer segments than workers, else one a worker
+  const int by_segment = segments <= workers;
+  cfg.gridDim = dim3(by_segment ? (unsigned)segments : workers, (frags + per - 1) / per);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, k_attn_join<TO, ES>, a, NT, par, Mma<T>::kOff) != cudaSuccess) return -1;
+  if (cudaLaunchKernelEx(&cfg, k_attn_join<TO, ES>, p, S::kLog, workers, by_segment, NT, par, Mma<T>::kOff) != cudaSuccess) return -1;
   moe_prof_count(2);
   return 0;
 }
