@@ -10,7 +10,7 @@
 #define MOE_DEV_ERR_BAD_SLOT 5u     // a slot is past the cache's last row
 
 // Most warps of the one-token attention kernel: its workspace holds two pieces for each.
-constexpr int MOE_ATTN_MAX_WORKERS = 1280;
+constexpr int MOE_ATTN_MAX_WORKERS = 1792;
 
 // Head width the kernel is compiled for that holds D, and the most head rows it takes at once.
 __host__ __device__ inline int moe_attn_width(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : (D <= 256 ? 256 : 512)); }

@@ -77,10 +77,10 @@ __device__ __forceinline__ uint32_t transposed8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {   // the low two bytes
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
-  return r;
+// The low and the high two bytes of v as fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t v, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(v));
 }
 // 16-byte asynchronous copy; with ok false nothing is read and zeros are written.
 __device__ __forceinline__ void copy16(uint32_t dst, const char *src, bool ok) {
@@ -109,7 +109,7 @@ template <int W, int NT, int ES> struct Shape {
   static constexpr int kUnit = kTok * kRow;         // bytes of its K or V rows
   // Slots of kUnit in a warp's ring: 96 KB a CTA, two CTAs an SM (192 KB and one where a slot is
   // 16 KB): at least 128 KB of copies in flight on an SM
-  static constexpr int kSlots = kUnit >= 16384 ? 3 : 24576 / kUnit;
+  static constexpr int kSlots = kUnit >= 16384 ? 3 : kUnit <= 4096 ? 4 : 24576 / kUnit;
   static constexpr int kRows = 8 * NT;
   static constexpr int kSmem = kWarps * kSlots * kUnit;
   static constexpr int kPieces = kRow / 16;         // 16-byte pieces of a row
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
   // ---- loader: runs ahead of the computation by the ring's slots, and its look-ups in the block
   // tables by two units more
   Cursor<S::kLog> ahead = at;   // the unit that is looked up next
-  int to_look_up = count, to_copy = count;
+  int to_look_up = count;
   struct Found {                // a looked-up unit, as lane r holds it for token r
     int page, in_page, kvh, first, last;   // tokens [first, last) of the unit are keys
   } now{}, then{};
@@ -438,78 +438,88 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
   int on[kParts];
 #pragma unroll
   for (int x = 0; x < kParts; ++x) on[x] = x * 512 + my_piece * 16 < p.D * ES;
-  int next = 0, slot_in = 0;   // copies are numbered K, V, K, V, ...
-  auto issue_next = [&]() {
-    const bool is_v = next & 1;
-    if (to_copy > 0) {
-      const char *base = is_v ? p.v : p.k;
-      if (!is_v) {
-        const int r = lane & (S::kTok - 1);
-        const bool good = (unsigned)now.page < (unsigned)p.num_pages;
-        if (!good) atomicCAS(p.err, 0u, MOE_DEV_ERR_BAD_PAGE);
-        off = (long long)now.kvh * p.head_b + (good ? (long long)now.page * p.page_b + (long long)now.in_page * p.tok_b : 0);
-        ok = good && r >= now.first && r < now.last;
-        all = p.groups_of_8 && __all_sync(kAll, ok);
-        if (p.groups_of_8) {
+  int slot_in = 0, left_k = count, left_v = count;   // copies are made K, V, K, V, ...
+  auto copy_unit = [&](const char *base) {
+    const uint32_t dst = ring + slot_in * S::kUnit;
+    const uint32_t to = dst + my_dst;   // its low bits hold the piece: slots are multiples of a row
+    if (all) {
+      // whole 8-token groups, each in one page: two additions and an XOR a copy
 #pragma unroll
-          for (int x = 0; x < S::kTok / 8; ++x) group[x] = __shfl_sync(kAll, off, 8 * x);
+      for (int x = 0; x < S::kTok / 8; ++x) {
+        const char *from = base + group[x] + my_off;
+#pragma unroll
+        for (int r = 0; r < 8; r += kPer) {
+          const char *row = from + (unsigned long long)(tok_b * (uint32_t)r);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part)
+            copy16_if((to ^ (uint32_t)(S::swz(r) << 4)) + (x * 8 + r) * S::kRow + part * 512, row + part * 512, on[part]);
         }
       }
-      const uint32_t dst = ring + slot_in * S::kUnit;
-      const uint32_t to = dst + my_dst;   // its low bits hold the piece: slots are multiples of a row
-      if (all) {
-        // whole 8-token groups, each in one page: two additions and an XOR a copy
-#pragma unroll
-        for (int x = 0; x < S::kTok / 8; ++x) {
-          const char *from = base + group[x] + my_off;
-#pragma unroll
-          for (int r = 0; r < 8; r += kPer) {
-            const char *row = from + (unsigned long long)(tok_b * (uint32_t)r);
-#pragma unroll
-            for (int part = 0; part < kParts; ++part)
-              copy16_if((to ^ (uint32_t)(S::swz(r) << 4)) + (x * 8 + r) * S::kRow + part * 512, row + part * 512, on[part]);
-          }
-        }
-      } else if (p.groups_of_8) {
-        // a sequence's or a window's end: rows that are no keys become zeros (0 x NaN in a page's
-        // unused rows would reach the output)
-        const unsigned rows = __ballot_sync(kAll, ok);
+    } else if (p.groups_of_8) {
+      // a sequence's or a window's end: rows that are no keys become zeros (0 x NaN in a page's
+      // unused rows would reach the output)
+      const unsigned rows = __ballot_sync(kAll, ok);
 #pragma unroll 1
-        for (int x = 0; x < S::kTok / 8; ++x) {
-          const char *from = base + __shfl_sync(kAll, off, 8 * x) + my_off;
+      for (int x = 0; x < S::kTok / 8; ++x) {
+        const char *from = base + __shfl_sync(kAll, off, 8 * x) + my_off;
 #pragma unroll
-          for (int r = 0; r < 8; r += kPer) {
-            const bool row_ok = rows >> (x * 8 + r + my_row) & 1;
-            const char *row = row_ok ? from + (unsigned long long)(tok_b * (uint32_t)r) : base;
+        for (int r = 0; r < 8; r += kPer) {
+          const bool row_ok = rows >> (x * 8 + r + my_row) & 1;
+          const char *row = row_ok ? from + (unsigned long long)(tok_b * (uint32_t)r) : base;
 #pragma unroll
-            for (int part = 0; part < kParts; ++part)
-              copy16((to ^ (uint32_t)(S::swz(r) << 4)) + (x * 8 + r) * S::kRow + part * 512, row + part * 512, row_ok && on[part]);
-          }
-        }
-      } else {
-#pragma unroll 4
-        for (int j = 0; j < S::kUnit / 512; ++j) {
-          const int idx = j * 32 + lane, r = idx / S::kPieces, ch = idx % S::kPieces;
-          const long long ro = __shfl_sync(kAll, off, r);
-          const bool row_ok = __shfl_sync(kAll, (int)ok, r) && ch * 16 < p.D * ES;
-          copy16(dst + r * S::kRow + ((ch ^ S::swz(r)) << 4), row_ok ? base + ro + ch * 16 : base, row_ok);
+          for (int part = 0; part < kParts; ++part)
+            copy16((to ^ (uint32_t)(S::swz(r) << 4)) + (x * 8 + r) * S::kRow + part * 512, row + part * 512, row_ok && on[part]);
         }
       }
-      if (is_v) {
-        --to_copy;
-        now = then;
-        look_up(then);
+    } else {
+#pragma unroll 2
+      for (int j = 0; j < S::kUnit / 512; ++j) {
+        const int idx = j * 32 + lane, r = idx / S::kPieces, ch = idx % S::kPieces;
+        const long long ro = __shfl_sync(kAll, off, r);
+        const bool row_ok = __shfl_sync(kAll, (int)ok, r) && ch * 16 < p.D * ES;
+        copy16(dst + r * S::kRow + ((ch ^ S::swz(r)) << 4), row_ok ? base + ro + ch * 16 : base, row_ok);
       }
     }
+  };
+  auto issue_k = [&]() {
+    if (left_k > 0) {
+      --left_k;
+      const int r = lane & (S::kTok - 1);
+      const bool good = (unsigned)now.page < (unsigned)p.num_pages;
+      if (!good) atomicCAS(p.err, 0u, MOE_DEV_ERR_BAD_PAGE);
+      off = (long long)now.kvh * p.head_b + (good ? (long long)now.page * p.page_b + (long long)now.in_page * p.tok_b : 0);
+      ok = good && r >= now.first && r < now.last;
+      all = p.groups_of_8 && __all_sync(kAll, ok);
+      if (all) {
+#pragma unroll
+        for (int x = 0; x < S::kTok / 8; ++x) group[x] = __shfl_sync(kAll, off, 8 * x);
+      }
+      now = then;
+      look_up(then);
+      copy_unit(p.k);
+    }
     copy_commit();
-    ++next;
+    slot_in = slot_in + 1 == S::kSlots ? 0 : slot_in + 1;
+  };
+  auto issue_v = [&]() {
+    if (left_v > 0) {
+      --left_v;
+      copy_unit(p.v);
+    }
+    copy_commit();
     slot_in = slot_in + 1 == S::kSlots ? 0 : slot_in + 1;
   };
   look_up(now);
   then = now;
   look_up(then);
+#pragma unroll 1
+  for (int x = 0; x < (S::kSlots - 1) / 2; ++x) {
+    issue_k();
+    issue_v();
+  }
+  if (S::kSlots % 2 == 0) issue_k();
 
-  int slot = 0, done = 0, lead = S::kSlots - 1;   // lead: copies issued before the first is waited for
+  int slot = 0, done = 0;
   while (true) {   // a piece: the units of one segment that are the warp's
     const int kvh = kv_head(p, at.seg), h0 = kvh * p.group + (at.seg - kvh * p.n_groups) * S::kRows;
     const int heads = min(S::kRows, (kvh + 1) * p.group - h0);
@@ -597,173 +607,170 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
 
     int t0 = at.token();
     uint32_t pf[S::kTiles][NT][2];   // P^T as B fragments
-    // One step a copy: K, V, K, V, ... (a single place that issues copies keeps the code small
-    // enough for the instruction cache)
+    load_q();
 #pragma unroll 1
-    for (int step = -lead; step < 2 * cnt; ++step) {
-      if (step >= 0) {
-        if (step == 0) load_q();
-        copy_wait<S::kSlots - 2>();
-        __syncwarp();
-        const uint32_t unit = ring + slot * S::kUnit;
-        if (!(step & 1)) {
-          // ---- S^T = K Q^T
-          constexpr int kAcc = S::kTiles == 1 ? 2 : 1;   // a single row tile takes two accumulators, to shorten the chain
-          float s[S::kTiles][NT][kAcc][4];
+    for (int i = 0; i < cnt; ++i, t0 += S::kTok) {
+      copy_wait<S::kSlots - 2>();
+      __syncwarp();
+      uint32_t unit = ring + slot * S::kUnit;
+      // ---- S^T = K Q^T
+      constexpr int kAcc = S::kTiles == 1 ? 2 : 1;   // a single row tile takes two accumulators, to shorten the chain
+      float s[S::kTiles][NT][kAcc][4];
+#pragma unroll
+      for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int x = 0; x < kAcc; ++x) s[t][n][x][e] = 0.f;
+      {
+        const int r = (lane & 7) + (lane & 8), hi = lane >> 4;
+        const uint32_t base = unit + r * S::kRow + ((hi ^ S::swz(r)) << 4);
+        if constexpr (ES == 2) {
+#pragma unroll
+          for (int k = 0; k < W / 16; ++k)
+#pragma unroll
+            for (int t = 0; t < S::kTiles; ++t) {
+              uint32_t a[4];
+              ldsm4(a, S::at(base, k) + t * 16 * S::kRow);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) M::run(s[t][n][k & (kAcc - 1)], a, qf[k][n][0], qf[k][n][1]);
+            }
+        } else {
+#pragma unroll
+          for (int k = 0; k < W / 32; ++k)
+#pragma unroll
+            for (int t = 0; t < S::kTiles; ++t) {
+              uint32_t w[4];
+              ldsm4(w, S::at(base, k) + t * 16 * S::kRow);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t a[4];
+                e4m3x4_to_f16x2(w[2 * h], a[0], a[2]);
+                e4m3x4_to_f16x2(w[2 * h + 1], a[1], a[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) M::run(s[t][n][h & (kAcc - 1)], a, qf[2 * k + h][n][0], qf[2 * k + h][n][1]);
+              }
+            }
+        }
+      }
+      slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+      __syncwarp();
+      // the freed slot takes the copy that is kSlots - 1 ahead
+      if constexpr (S::kSlots % 2) issue_k();
+      else issue_v();
+
+      // ---- softmax over the unit's tokens, in base 2
+      const bool full = t0 >= at.sp.lo && t0 + S::kTok <= at.sp.len;   // every token of the unit is a key
+      bool scale_o = false;
+      float al[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float v[S::kTiles][4];
+#pragma unroll
+        for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[t][e] = (kAcc == 2 ? s[t][n][0][e] + s[t][n][kAcc - 1][e] : s[t][n][0][e]) * sc[n][e & 1];
+        if (!full) {
 #pragma unroll
           for (int t = 0; t < S::kTiles; ++t)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int x = 0; x < kAcc; ++x) s[t][n][x][e] = 0.f;
-          {
-                    const int r = (lane & 7) + (lane & 8), hi = lane >> 4;
-            const uint32_t base = unit + r * S::kRow + ((hi ^ S::swz(r)) << 4);
-            if constexpr (ES == 2) {
-#pragma unroll
-              for (int k = 0; k < W / 16; ++k)
-#pragma unroll
-                for (int t = 0; t < S::kTiles; ++t) {
-                  uint32_t a[4];
-                  ldsm4(a, S::at(base, k) + t * 16 * S::kRow);
-#pragma unroll
-                  for (int n = 0; n < NT; ++n) M::run(s[t][n][k & (kAcc - 1)], a, qf[k][n][0], qf[k][n][1]);
-                }
-            } else {
-#pragma unroll
-              for (int k = 0; k < W / 32; ++k)
-#pragma unroll
-                for (int t = 0; t < S::kTiles; ++t) {
-                  uint32_t w[4];
-                  ldsm4(w, S::at(base, k) + t * 16 * S::kRow);
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    uint32_t a[4];
-                    a[0] = e4m3x2_to_f16x2(w[2 * h]);
-                    a[1] = e4m3x2_to_f16x2(w[2 * h + 1]);
-                    a[2] = e4m3x2_to_f16x2(w[2 * h] >> 16);
-                    a[3] = e4m3x2_to_f16x2(w[2 * h + 1] >> 16);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) M::run(s[t][n][h & (kAcc - 1)], a, qf[2 * k + h][n][0], qf[2 * k + h][n][1]);
-                  }
-                }
+            for (int e = 0; e < 4; ++e) {
+              const int tok = t0 + g + 16 * t + 8 * (e >> 1);
+              if (tok < at.sp.lo || tok >= at.sp.len) v[t][e] = ninf;
             }
-          }
-
-          // ---- softmax over the unit's tokens, in base 2
-          const bool full = t0 >= at.sp.lo && t0 + S::kTok <= at.sp.len;   // every token of the unit is a key
-          bool scale_o = false;
-          float al[NT][2];
+        }
+        float m0 = fmaxf(v[0][0], v[0][2]), m1 = fmaxf(v[0][1], v[0][3]);
+#pragma unroll
+        for (int t = 1; t < S::kTiles; ++t) {
+          m0 = fmaxf(m0, fmaxf(v[t][0], v[t][2]));
+          m1 = fmaxf(m1, fmaxf(v[t][1], v[t][3]));
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
+          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
+        }
+        m0 = fmaxf(m0, mx[n][0]);
+        m1 = fmaxf(m1, mx[n][1]);
+        // a maximum of -inf (no key yet) must not meet itself in a difference
+        const float b0 = (m0 == ninf ? 0.f : m0) - M::kOff, b1 = (m1 == ninf ? 0.f : m1) - M::kOff;
+        al[n][0] = exp2_fast(mx[n][0] - M::kOff - b0);
+        al[n][1] = exp2_fast(mx[n][1] - M::kOff - b1);
+        scale_o |= m0 != mx[n][0] || m1 != mx[n][1];
+        mx[n][0] = m0;
+        mx[n][1] = m1;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int t = 0; t < S::kTiles; ++t) {
+          const float p0 = exp2_fast(v[t][0] - b0), p1 = exp2_fast(v[t][1] - b1), p2 = exp2_fast(v[t][2] - b0), p3 = exp2_fast(v[t][3] - b1);
+          s0 += p0 + p2;
+          s1 += p1 + p3;
+          pf[t][n][0] = transposed8x8(M::pack(p0, p1));
+          pf[t][n][1] = transposed8x8(M::pack(p2, p3));
+        }
+        l[n][0] = fmaf(l[n][0], al[n][0], s0);
+        l[n][1] = fmaf(l[n][1], al[n][1], s1);
+      }
+      if (__any_sync(0xffffffffu, scale_o)) {
+#pragma unroll
+        for (int k = 0; k < W / 16; ++k)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float v[S::kTiles][4];
-#pragma unroll
-            for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[t][e] = (kAcc == 2 ? s[t][n][0][e] + s[t][n][kAcc - 1][e] : s[t][n][0][e]) * sc[n][e & 1];
-            if (!full) {
-#pragma unroll
-              for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int tok = t0 + g + 16 * t + 8 * (e >> 1);
-                  if (tok < at.sp.lo || tok >= at.sp.len) v[t][e] = ninf;
-                }
-            }
-            float m0 = fmaxf(v[0][0], v[0][2]), m1 = fmaxf(v[0][1], v[0][3]);
-#pragma unroll
-            for (int t = 1; t < S::kTiles; ++t) {
-              m0 = fmaxf(m0, fmaxf(v[t][0], v[t][2]));
-              m1 = fmaxf(m1, fmaxf(v[t][1], v[t][3]));
-            }
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-              m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
-              m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
-            }
-            m0 = fmaxf(m0, mx[n][0]);
-            m1 = fmaxf(m1, mx[n][1]);
-            // a maximum of -inf (no key yet) must not meet itself in a difference
-            const float b0 = (m0 == ninf ? 0.f : m0) - M::kOff, b1 = (m1 == ninf ? 0.f : m1) - M::kOff;
-            al[n][0] = exp2_fast(mx[n][0] - M::kOff - b0);
-            al[n][1] = exp2_fast(mx[n][1] - M::kOff - b1);
-            scale_o |= m0 != mx[n][0] || m1 != mx[n][1];
-            mx[n][0] = m0;
-            mx[n][1] = m1;
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int t = 0; t < S::kTiles; ++t) {
-              const float p0 = exp2_fast(v[t][0] - b0), p1 = exp2_fast(v[t][1] - b1), p2 = exp2_fast(v[t][2] - b0), p3 = exp2_fast(v[t][3] - b1);
-              s0 += p0 + p2;
-              s1 += p1 + p3;
-              pf[t][n][0] = transposed8x8(M::pack(p0, p1));
-              pf[t][n][1] = transposed8x8(M::pack(p2, p3));
-            }
-            l[n][0] = fmaf(l[n][0], al[n][0], s0);
-            l[n][1] = fmaf(l[n][1], al[n][1], s1);
+            o[k][n][0] *= al[n][0];
+            o[k][n][1] *= al[n][1];
+            o[k][n][2] *= al[n][0];
+            o[k][n][3] *= al[n][1];
           }
-          if (__any_sync(0xffffffffu, scale_o)) {
-#pragma unroll
-            for (int k = 0; k < W / 16; ++k)
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                o[k][n][0] *= al[n][0];
-                o[k][n][1] *= al[n][1];
-                o[k][n][2] *= al[n][0];
-                o[k][n][3] *= al[n][1];
-              }
-          }
-        } else {
-          // ---- O^T += V^T P^T
-          {
-                    if constexpr (ES == 2) {
-              const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
-              const uint32_t base = unit + r * S::kRow + ((hi ^ S::swz(r)) << 4);
-#pragma unroll
-              for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-                for (int k = 0; k < W / 16; ++k) {
-                  uint32_t a[4];
-                  ldsm4t(a, S::at(base, k) + t * 16 * S::kRow);
-#pragma unroll
-                  for (int n = 0; n < NT; ++n) M::run(o[k][n], a, pf[t][n][0], pf[t][n][1]);
-                }
-            } else {
-              const int r = (lane & 7) + (lane & 8), hi = lane >> 4;
-              const uint32_t base = unit + r * S::kRow + ((hi ^ S::swz(r)) << 4);
-#pragma unroll
-              for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-                for (int k = 0; k < W / 32; ++k) {
-                  uint32_t w[4];
-                  ldsm4t(w, S::at(base, k) + t * 16 * S::kRow);
-                  // a word holds elements (2g, 2g + 1) of token 2c, then of token 2c + 1: row g of the
-                  // product's tile takes element 2g, row g + 8 element 2g + 1
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const uint32_t lo = __byte_perm(w[2 * h], 0u, 0x3120), hi8 = __byte_perm(w[2 * h + 1], 0u, 0x3120);
-                    uint32_t a[4];
-                    a[0] = e4m3x2_to_f16x2(lo);
-                    a[1] = e4m3x2_to_f16x2(lo >> 16);
-                    a[2] = e4m3x2_to_f16x2(hi8);
-                    a[3] = e4m3x2_to_f16x2(hi8 >> 16);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) M::run(o[2 * k + h][n], a, pf[t][n][0], pf[t][n][1]);
-                  }
-                }
-            }
-          }
-          t0 += S::kTok;
-        }
-        slot = slot + 1 == S::kSlots ? 0 : slot + 1;
-        __syncwarp();
       }
-      issue_next();
+
+      copy_wait<S::kSlots - 2>();
+      __syncwarp();
+      unit = ring + slot * S::kUnit;
+      // ---- O^T += V^T P^T
+      {
+        if constexpr (ES == 2) {
+          const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
+          const uint32_t base = unit + r * S::kRow + ((hi ^ S::swz(r)) << 4);
+#pragma unroll
+          for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+            for (int k = 0; k < W / 16; ++k) {
+              uint32_t a[4];
+              ldsm4t(a, S::at(base, k) + t * 16 * S::kRow);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) M::run(o[k][n], a, pf[t][n][0], pf[t][n][1]);
+            }
+        } else {
+          const int r = (lane & 7) + (lane & 8), hi = lane >> 4;
+          const uint32_t base = unit + r * S::kRow + ((hi ^ S::swz(r)) << 4);
+#pragma unroll
+          for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+            for (int k = 0; k < W / 32; ++k) {
+              uint32_t w[4];
+              ldsm4t(w, S::at(base, k) + t * 16 * S::kRow);
+              // a word holds elements (2g, 2g + 1) of token 2c, then of token 2c + 1: row g of the
+              // product's tile takes element 2g, row g + 8 element 2g + 1
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t lo = __byte_perm(w[2 * h], 0u, 0x3120), hi8 = __byte_perm(w[2 * h + 1], 0u, 0x3120);
+                uint32_t a[4];
+                e4m3x4_to_f16x2(lo, a[0], a[1]);
+                e4m3x4_to_f16x2(hi8, a[2], a[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) M::run(o[2 * k + h][n], a, pf[t][n][0], pf[t][n][1]);
+              }
+            }
+        }
+      }
+      slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+      __syncwarp();
+      if constexpr (S::kSlots % 2) issue_v();
+      else issue_k();
     }
-    lead = 0;
 
     // ---- the piece's result
     done += cnt;
