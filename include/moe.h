@@ -321,7 +321,7 @@ typedef struct moe_heads {
  *               where n_q = 0). Each may be its own input (same base and strides).
  *   cache, layer, slots  NULL, or the cache that k (rotated) and v are stored in: token t in row
  *               slots[t] % page_size of page slots[t] / page_size (device int64 [T]; negative:
- *               not stored). Its dtype is dtype or MOE_DT_E4M3 (value / scale, saturated at
+ *               not stored). Its dtype is dtype or MOE_DT_E4M3 (value times 1 / scale in FP32, saturated at
  *               +-448). Slots that are not negative must be distinct: of tokens with the same
  *               slot, which one's values remain is not defined.
  * Sums and products in FP32, rounded once. T = 0 is a no-op.

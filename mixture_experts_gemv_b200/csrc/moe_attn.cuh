@@ -53,13 +53,13 @@ struct RopeParams {
   const int32_t *positions;
   const double *inv_freq;
   const float *q_gain, *k_gain;
-  float eps, rope_scale;
+  float eps, rope_scale, inv_d;                             // inv_d: 1 / D
   int T, nq, nkv, D, rot;
   char *ck, *cv;                           // cache, or null
   long long page_b, tok_b, head_b;         // bytes
   long long n_slots;
   int page_size;
-  float k_scale, v_scale;
+  float inv_k_scale, inv_v_scale;
   const int64_t *slots;
   uint32_t *err;
 };

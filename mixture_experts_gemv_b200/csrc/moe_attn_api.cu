@@ -148,7 +148,7 @@ int moe_qk_norm_rope(const moe_heads *q, const moe_heads *k, const moe_heads *v,
                      float rope_scale, const float *q_gain, const float *k_gain, float eps, const moe_heads *q_out,
                      const moe_heads *k_out, const moe_kv_cache *cache, int layer, const int64_t *slots, void *stream) {
   if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16) return fail(MOE_ERR_BAD_ARG, "dtype %d is neither bf16 nor fp16", dtype);
-  if (T < 0 || n_q < 0 || n_kv < 0 || n_q + n_kv == 0 || n_q > 65536 || n_kv > 65536)
+  if (T < 0 || n_q < 0 || n_kv < 0 || n_q + n_kv == 0 || n_q > 4096 || n_kv > 4096)
     return fail(MOE_ERR_BAD_ARG, "bad shape T = %d, n_q = %d, n_kv = %d", T, n_q, n_kv);
   int rc = check_head_dim(head_dim);
   if (rc) return rc;
@@ -230,6 +230,7 @@ int moe_qk_norm_rope(const moe_heads *q, const moe_heads *k, const moe_heads *v,
   p.nkv = n_kv;
   p.D = head_dim;
   p.rot = rotary_dim;
+  p.inv_d = 1.f / (float)head_dim;
   bool f8 = false;
   if (cache) {
     const int es = element_bytes(cache->dtype);
@@ -242,8 +243,8 @@ int moe_qk_norm_rope(const moe_heads *q, const moe_heads *k, const moe_heads *v,
     p.head_b = cache->head_stride * es;
     p.n_slots = (long long)cache->num_pages * cache->page_size;
     p.page_size = cache->page_size;
-    p.k_scale = cache->k_scale;
-    p.v_scale = cache->v_scale;
+    p.inv_k_scale = (float)(1.0 / cache->k_scale);
+    p.inv_v_scale = (float)(1.0 / cache->v_scale);
     p.slots = slots;
   }
   p.err = dev->err;
@@ -306,7 +307,7 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
   if (!rc) rc = check_heads(q, "q");
   if (!rc) rc = check_heads(out, "out");
   if (rc) return rc;
-  if (B < 0 || n_q < 1 || n_q % cache->n_kv || n_q > 65536)
+  if (B < 0 || n_q < 1 || n_q % cache->n_kv || n_q > 4096)
     return fail(MOE_ERR_BAD_ARG, "bad shape B = %d, n_q = %d over n_kv = %d", B, n_q, cache->n_kv);
   if (max_pages < 1 || table_stride < max_pages || (long long)max_pages * cache->page_size > (1ll << 30))
     return fail(MOE_ERR_BAD_ARG, "max_pages = %d (rows %lld apart) of %d tokens: need 1 <= max_pages <= table_stride and at "

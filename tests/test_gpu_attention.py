@@ -430,6 +430,47 @@ def test_rope_in_place_and_outputs_alone():
     assert torch.equal(q, qo) and torch.equal(k, ko) and torch.equal(v, v0)
 
 
+@pytest.mark.parametrize("cache_dtype", [BF, E4])
+def test_rope_heads_and_tokens_apart(cache_dtype):
+    """Heads that are not neighbours, wide tokens, more heads than one block takes; what is between stays."""
+    g = gen(12)
+    T, nq, nkv, D = 21, 70, 9, 96
+    wide = normal((T, nq + 2 * nkv + 3, D + 16), BF, g)
+    q, k, v = wide[:, 1: 1 + nq, :D], wide[:, nq + 1: nq + 1 + nkv, :D], wide[:, nq + nkv + 2: nq + 2 * nkv + 2, 16:]
+    outs = torch.full((T, nq + nkv + 1, D + 8), 7.0, device=DEV, dtype=BF)
+    q_out, k_out = outs[:, :nq, :D], outs[:, nq + 1:, :D]
+    pos = torch.arange(T, device=DEV, dtype=torch.int32) * 11
+    inv, _ = moe.moe_rope_frequencies(64, device=DEV)
+    qg, kg = (torch.randn(D, generator=g, device=DEV) for _ in range(2))
+    kv = torch.zeros((2, 5, 9, nkv + 2, D + 32), device=DEV, dtype=torch.float32).to(cache_dtype)
+    cache = moe.MoeKvCache(kv[0, :, 1:6, :nkv, 16: 16 + D], kv[1, :, 1:6, :nkv, 16: 16 + D], "NHD",
+                           *((0.05, 0.04) if cache_dtype == E4 else (1.0, 1.0)))
+    slots = torch.randperm(25, generator=g, device=DEV)[:T]
+    before = wide.clone()
+    moe.moe_qk_norm_rope(q, k, v, pos, inv, q_gain=qg, k_gain=kg, q_out=q_out, k_out=k_out, cache=cache, slots=slots)
+    moe.moe_cache_check()
+    assert torch.equal(wide, before)
+    for x, gain, out in ((q, qg, q_out), (k, kg, k_out)):
+        want, size = ref.rotated(x, gain, 1e-6, pos, inv, False)
+        assert ((out.double() - want).abs() <= ref.rotated_bound(want, size, D, BF)).all()
+    want, size = ref.rotated(k, kg, 1e-6, pos, inv, False)
+    got = ref.cache_rows(cache, 0, "k", slots // 5, slots % 5)
+    assert ((got - want).abs() <= ref.rotated_bound(want, size, D, cache_dtype, cache.k_scale)).all()
+    got = ref.cache_rows(cache, 0, "v", slots // 5, slots % 5)
+    assert ((got - v.double()).abs() <= ref.rotated_bound(v.double(), v.double().abs(), D, cache_dtype, cache.v_scale)).all()
+    left = outs.clone()
+    left[:, :nq, :D] = 7.0
+    left[:, nq + 1:, :D] = 7.0
+    assert (left == 7.0).all()
+    raw = kv.view(torch.uint8)
+    es = 1 if cache_dtype == E4 else 2
+    held = torch.zeros(raw.shape, dtype=torch.bool, device=DEV)
+    for i in range(2):
+        part = held[i, :, 1:6, :nkv, 16 * es: (16 + D) * es]
+        part[slots // 5, slots % 5] = True
+    assert (raw[~held] == 0).all()
+
+
 def test_rope_infinities_stay_in_their_pairs():
     """Without a norm an infinity reaches its rotation partner alone, and none beyond rotary_dim."""
     for inter in (False, True):
