@@ -8,6 +8,7 @@ of the library if libmoe.so has not been built: there is no other implementation
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -321,28 +322,31 @@ def _dtype_code(dtype) -> int:
     return code
 
 
-def _need(t, name, dtype, shape, device):
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        _refuse(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+def _need(t, name, dtype, shape, index):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {_place(index)}, "
                 f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-def _heads(t, name, shape, dtype, device):
+def _heads(t, name, shape, dtype, index):
     """moe_heads of a [T, heads, head_dim] tensor."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
-        _refuse(f"{name}: need {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(f"{name}: need {dtype} {tuple(shape)} on {_place(index)}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     token, head, one = t.stride()
     if one != 1:
         _refuse(f"{name}: the elements of a head must be contiguous")
     return _HEADS.pack(t.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0)
 
 
-def _call(fn, device, stream, *args):
+def _place(index):
+    return "the CPU" if index < 0 else f"cuda:{index}"
+
+
+def _call(fn, index, stream, *args):
     """fn(*args, stream) with the tensors' device current; stream None: its current stream."""
-    index = device.index
-    if device.type != "cuda":
-        _refuse(f"tensors must be on a CUDA device, not {device}")
+    if index < 0:
+        _refuse("tensors must be on a CUDA device, not on the CPU")
     if stream is None:
         stream = _raw_stream(index)
     elif not isinstance(stream, int):
@@ -350,7 +354,7 @@ def _call(fn, device, stream, *args):
     if _torch._C._cuda_getDevice() == index:
         rc = fn(*args, stream)
     else:
-        with _torch.cuda.device(device):
+        with _torch.cuda.device(index):
             rc = fn(*args, stream)
     if rc != MOE_OK:
         _check(rc)
@@ -379,7 +383,7 @@ class MoeKvCache:
             _refuse(f"unknown layout {layout!r}")
         if one != 1 and dim > 1:
             _refuse("the elements of a head must be contiguous")
-        self.k, self.v, self.layout, self.device, self.dtype = k, v, layout, k.device, k.dtype
+        self.k, self.v, self.layout, self.index, self.dtype = k, v, layout, k.get_device(), k.dtype
         self.n_layers, self.num_pages, self.page_size, self.n_kv, self.head_dim = layers, pages, tokens, heads, dim
         self.k_scale, self.v_scale = k_scale, v_scale
         # the stride of a dimension of one is not used and may be anything
@@ -400,13 +404,23 @@ def moe_qk_norm_rope(q, k, v, positions, inv_freq, q_gain=None, k_gain=None, eps
     if some is None or some.dim() != 3 or (k is not None and k.dim() != 3):
         _refuse("q or k of shape [T, heads, head_dim] needed")
     T, _, D = some.shape
-    dev, dt = some.device, some.dtype
-    n_q = 0 if q is None else q.shape[1]
-    n_kv = 0 if k is None else k.shape[1]
-    of_q, of_k = (T, n_q, D), (T, n_kv, D)
-    ph = [None if t is None else _heads(t, name, shape, dt, dev)
-          for t, name, shape in ((q, "q", of_q), (k, "k", of_k), (None if cache is None else v, "v", of_k),
-                                 (q_out, "q_out", of_q), (k_out, "k_out", of_k))]
+    dev, dt = some.get_device(), some.dtype
+    n_q = n_kv = 0
+    pq = pk = pv = pq_out = pk_out = None
+    if q is not None:
+        of_q = q.shape
+        n_q = of_q[1]
+        pq = _heads(q, "q", of_q, dt, dev)
+        if q_out is not None:
+            pq_out = _heads(q_out, "q_out", of_q, dt, dev)
+    if k is not None:
+        n_kv = k.shape[1]
+        of_k = (T, n_kv, D)
+        pk = _heads(k, "k", of_k, dt, dev)
+        if k_out is not None:
+            pk_out = _heads(k_out, "k_out", of_k, dt, dev)
+        if cache is not None and v is not None:
+            pv = _heads(v, "v", of_k, dt, dev)
     rot, p_pos, p_freq = 0, None, None
     if inv_freq is not None:
         half = inv_freq.numel()
@@ -419,8 +433,8 @@ def moe_qk_norm_rope(q, k, v, positions, inv_freq, q_gain=None, k_gain=None, eps
     p_kg = None if k_gain is None else _need(k_gain, "k_gain", _torch.float32, (D,), dev)
     packed = p_slots = None
     if cache is not None:
-        if cache.device != dev:
-            _refuse(f"the cache is on {cache.device}, q and k on {dev}")
+        if cache.index != dev:
+            _refuse(f"the cache is on {_place(cache.index)}, q and k on {_place(dev)}")
         if slots is None:
             _refuse("slots needed with a cache")
         p_slots = _need(slots, "slots", _torch.int64, (T,), dev)
@@ -428,8 +442,8 @@ def moe_qk_norm_rope(q, k, v, positions, inv_freq, q_gain=None, k_gain=None, eps
     code = _dtype_code(dt)
     if T == 0:
         return
-    _call(lib().moe_qk_norm_rope, dev, stream, ph[0], ph[1], ph[2], code, T, n_q, n_kv, D, p_pos, p_freq, rot,
-          1 if interleaved else 0, rope_scale, p_qg, p_kg, eps, ph[3], ph[4], packed, layer, p_slots)
+    _call(lib().moe_qk_norm_rope, dev, stream, pq, pk, pv, code, T, n_q, n_kv, D, p_pos, p_freq, rot,
+          1 if interleaved else 0, rope_scale, p_qg, p_kg, eps, pq_out, pk_out, packed, layer, p_slots)
 
 
 def moe_rope_frequencies(rotary_dim: int, base: float = 10000.0, kind: int = MOE_ROPE_PLAIN, factor: float = 1.0,
@@ -444,6 +458,11 @@ def moe_rope_frequencies(rotary_dim: int, base: float = 10000.0, kind: int = MOE
     return (out if device is None else out.to(device)), scale.value
 
 
+@functools.lru_cache(maxsize=64)
+def _workspace_bytes(n_q, n_kv, head_dim):
+    return int(lib().moe_attention_decode_workspace_bytes(n_q, n_kv, head_dim))
+
+
 def moe_attention_decode_workspace_bytes(n_q: int, n_kv: int, head_dim: int) -> int:
     return int(lib().moe_attention_decode_workspace_bytes(n_q, n_kv, head_dim))
 
@@ -456,14 +475,14 @@ def moe_attention_decode(q, cache: MoeKvCache, block_tables, seq_lens, out, scal
     the stream's own memory pool, a captured graph's under capture)."""
     if q.dim() != 3:
         _refuse("q of shape [B, n_q, head_dim] needed")
-    shape, dev, dt = q.shape, q.device, q.dtype
+    shape, dev, dt = q.shape, q.get_device(), q.dtype
     B, n_q, D = shape
-    if D != cache.head_dim or cache.device != dev:
-        _refuse(f"q of {D} on {dev} over a cache of {cache.head_dim} on {cache.device}")
-    ph_q = _heads(q, "q", shape, dt, dev)
-    ph_out = _heads(out, "out", shape, dt, dev)
-    if block_tables.dim() != 2 or block_tables.dtype != _torch.int32 or block_tables.device != dev:
-        _refuse(f"block_tables: need int32 [{B}, max_pages] on {dev}")
+    if D != cache.head_dim or cache.index != dev:
+        _refuse(f"q of {D} on {_place(dev)} over a cache of {cache.head_dim} on {_place(cache.index)}")
+    pq = _heads(q, "q", shape, dt, dev)
+    pout = _heads(out, "out", shape, dt, dev)
+    if block_tables.dim() != 2 or block_tables.dtype is not _torch.int32 or block_tables.get_device() != dev:
+        _refuse(f"block_tables: need int32 [{B}, max_pages] on {_place(dev)}")
     rows, cols = block_tables.shape
     table_st, one = block_tables.stride()
     if rows != B or (one != 1 and cols > 1):
@@ -475,19 +494,21 @@ def moe_attention_decode(q, cache: MoeKvCache, block_tables, seq_lens, out, scal
         return
     L = lib()
     if workspace is None:
-        size = L.moe_attention_decode_workspace_bytes(n_q, cache.n_kv, D)
-        if stream is None or dev.type != "cuda":
-            workspace = _torch.empty(size, dtype=_torch.uint8, device=dev)
+        size = _workspace_bytes(n_q, cache.n_kv, D)
+        if dev < 0:
+            _refuse("tensors must be on a CUDA device, not on the CPU")
+        if stream is None:
+            workspace = _torch.empty(size, dtype=_torch.uint8, device=q.device)
         else:   # from the pool of the stream that will use it
-            s = _torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+            s = _torch.cuda.ExternalStream(stream, device=q.device) if isinstance(stream, int) else stream
             with _torch.cuda.stream(s):
-                workspace = _torch.empty(size, dtype=_torch.uint8, device=dev)
+                workspace = _torch.empty(size, dtype=_torch.uint8, device=q.device)
     else:
-        if workspace.device != dev or not workspace.is_contiguous():
-            _refuse(f"workspace: need a contiguous tensor on {dev}")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse(f"workspace: need a contiguous tensor on {_place(dev)}")
         size = workspace.numel() * workspace.element_size()
-    _call(L.moe_attention_decode, dev, stream, ph_q, code, cache.packed, layer, block_tables.data_ptr(),
-          table_st if B > 1 else cols, cols, p_lens, B, n_q, scale, window, ph_out, p_lse, workspace.data_ptr(), size)
+    _call(L.moe_attention_decode, dev, stream, pq, code, cache.packed, layer, block_tables.data_ptr(),
+          table_st if B > 1 else cols, cols, p_lens, B, n_q, scale, window, pout, p_lse, workspace.data_ptr(), size)
 
 
 def _host_pages(v, name):
@@ -509,8 +530,8 @@ def moe_copy_pages(cache: MoeKvCache, src, dst, block_tables=None, stream=None) 
     rows = cols = table_st = 0
     p_tables = None
     if block_tables is not None:
-        if block_tables.dim() != 2 or block_tables.dtype != _torch.int32 or block_tables.device != cache.device:
-            _refuse(f"block_tables: need int32 [rows, cols] on {cache.device}")
+        if block_tables.dim() != 2 or block_tables.dtype is not _torch.int32 or block_tables.get_device() != cache.index:
+            _refuse(f"block_tables: need int32 [rows, cols] on {_place(cache.index)}")
         rows, cols = block_tables.shape
         table_st, one = block_tables.stride()
         if one != 1 and cols > 1:
@@ -520,7 +541,7 @@ def moe_copy_pages(cache: MoeKvCache, src, dst, block_tables=None, stream=None) 
         p_tables = block_tables.data_ptr()
     if n == 0:
         return
-    _call(lib().moe_copy_pages, cache.device, stream, cache.packed, src.data_ptr(), dst.data_ptr(), n, p_tables,
+    _call(lib().moe_copy_pages, cache.index, stream, cache.packed, src.data_ptr(), dst.data_ptr(), n, p_tables,
           table_st, rows, cols)
 
 
@@ -529,6 +550,6 @@ def moe_cache_check(device=None, stream=None) -> None:
     if _torch is None:
         _setup()
     dev = _torch.device("cuda" if device is None else device)
-    if dev.type == "cuda" and dev.index is None:
-        dev = _torch.device("cuda", _torch.cuda.current_device())
-    _call(lib().moe_cache_check, dev, stream)
+    if dev.type != "cuda":
+        _refuse(f"{dev} is not a CUDA device")
+    _call(lib().moe_cache_check, _torch.cuda.current_device() if dev.index is None else dev.index, stream)

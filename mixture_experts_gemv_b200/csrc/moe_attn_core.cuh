@@ -906,32 +906,18 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
         if (j + x * par < pieces.count) sum.take(m[x], v[x]);
     }
   }
-  if (par > 1) {
+  // groups of up to four join at a time: 16 -> 4 -> 1
+  for (int groups = par; groups > 1; groups = (groups + 3) / 4) {
     s_acc[tid] = sum.acc;
     s_ml[tid] = sum.ml;
     __syncthreads();
-    if (j0) return;
-    // the maximum first, so that the groups' exponentials do not wait for one another
-    const float ninf = __int_as_float(0xff800000);
-    float m0 = sum.ml.x, m1 = sum.ml.z;
-    for (int j = 1; j < par; ++j) {
-      m0 = fmaxf(m0, s_ml[j * per + tid].x);
-      m1 = fmaxf(m1, s_ml[j * per + tid].z);
+    const int keep = (groups + 3) / 4;
+    if (j0 < keep) {
+      for (int j = j0 + keep; j < groups; j += keep) sum.take(s_ml[tid + (j - j0) * per], s_acc[tid + (j - j0) * per]);
     }
-    const float b0 = m0 == ninf ? 0.f : m0, b1 = m1 == ninf ? 0.f : m1;
-    float l0 = 0.f, l1 = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int j = 0; j < par; ++j) {
-      const float4 ml = s_ml[j * per + tid], v = s_acc[j * per + tid];
-      const float f0 = exp2_fast(ml.x - b0), f1 = exp2_fast(ml.z - b1);
-      l0 = fmaf(f0, ml.y, l0);
-      l1 = fmaf(f1, ml.w, l1);
-      a = make_float4(fmaf(f0, v.x, a.x), fmaf(f1, v.y, a.y), fmaf(f0, v.z, a.z), fmaf(f1, v.w, a.w));
-    }
-    sum.ml = make_float4(m0, l0, m1, l1);
-    sum.acc = a;
+    __syncthreads();
   }
+  if (j0) return;
   if (f - lane >= frags) return;   // whole warps
   TO *out = static_cast<TO *>(p.out) + (long long)b * p.out_tok + (long long)h0 * p.out_head;
   store_fragment<TO, ES>(out, p.out_head, k, heads, lane, sum.acc, sum.ml.y == 0.f ? 0.f : p.v_scale / sum.ml.y,
