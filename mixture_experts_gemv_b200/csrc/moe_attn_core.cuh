@@ -855,6 +855,7 @@ constexpr int kJoinPar = 16;     // groups
 template <typename TO, int ES>
 __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int log, int all_workers, int by_segment, int nt, int par, float off) {
   __shared__ float4 s_acc[kJoinMost], s_ml[kJoinMost];
+  pdl_launch_dependents();   // what comes next may be made ready; it waits for this kernel's end
   int w0, w1, b, seg;
   bool joined;
   {
@@ -945,17 +946,8 @@ template <typename T, int W, int NT, int ES, bool QB> int launch(const AttnParam
   if (grid * kWarps > MOE_ATTN_MAX_WORKERS) grid = MOE_ATTN_MAX_WORKERS / kWarps;
   const long long segments = (long long)p.B * p.nkv * p.n_groups;
   const int workers = grid * kWarps;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) return -1;
+  PdlLaunch l(dim3(grid), kWarps * 32, S::kSmem, s);
+  if (cudaLaunchKernelEx(&l.cfg, fn, p) != cudaSuccess) return -1;
   // Threads that share a fragment in the join: as many as a quarter of the pieces that a segment
   // has when all are equally long and blocks join theirs, so that each one's loads are in flight
   // together
@@ -964,10 +956,8 @@ template <typename T, int W, int NT, int ES, bool QB> int launch(const AttnParam
   const int threads = par > 4 ? kJoinMost : kJoinMost / 2, frags = p.D / 16 * NT * 32, per = threads / par;
   // a block a segment where there are fewer segments than workers, else one a worker
   const int by_segment = segments <= workers;
-  cfg.gridDim = dim3(by_segment ? (unsigned)segments : workers, (frags + per - 1) / per);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, k_attn_join<TO, ES>, p, S::kLog, workers, by_segment, NT, par, Mma<T>::kOff) != cudaSuccess) return -1;
+  PdlLaunch j(dim3(by_segment ? (unsigned)segments : workers, (frags + per - 1) / per), threads, 0, s);
+  if (cudaLaunchKernelEx(&j.cfg, k_attn_join<TO, ES>, p, S::kLog, workers, by_segment, NT, par, Mma<T>::kOff) != cudaSuccess) return -1;
   moe_prof_count(2);
   return 0;
 }

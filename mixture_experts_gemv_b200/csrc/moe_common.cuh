@@ -228,6 +228,24 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 
 // ---------------------------------------------------------------- host-side launch helpers
 
+// A launch that may be made ready before the kernel in front of it in the stream has ended
+// (programmatic stream serialization): its kernel calls pdl_wait() before it touches memory.
+struct PdlLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  PdlLaunch(dim3 grid, unsigned threads, size_t smem, cudaStream_t s) {
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  PdlLaunch(const PdlLaunch &) = delete;
+};
+
 struct MoeLaunch {
   cudaStream_t stream;
   bool pdl;                 // launch with programmatic stream serialization

@@ -20,9 +20,11 @@ template <int N> struct Pairs {
 };
 
 template <int N, bool DENSE>
-__global__ void __launch_bounds__(kThreads) k_copy_pages(const CopyParams p, const __grid_constant__ Pairs<N> list) {
+__global__ void __launch_bounds__(kThreads) k_copy_pages(const __grid_constant__ CopyParams p, const __grid_constant__ Pairs<N> list) {
   const int tid = threadIdx.x;
   long long block = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
   if (block < p.table_blocks) {
     __shared__ int src[N];
     for (int i = tid; i < p.n; i += kThreads) src[i] = list.v[i].x;
@@ -79,8 +81,8 @@ template <int N, bool DENSE> int launch_part(CopyParams p, const int2 *pairs, cu
   p.stretches = (int)((p.pieces + kThreads * kPer - 1) / (kThreads * kPer));
   const long long blocks = p.table_blocks + (long long)p.stretches * p.n * p.layers * 2;
   if (blocks > 0x7fffffffll) return -2;
-  k_copy_pages<N, DENSE><<<(unsigned)blocks, kThreads, 0, s>>>(p, list);
-  if (cudaGetLastError() != cudaSuccess) return -1;
+  PdlLaunch l(dim3((unsigned)blocks), kThreads, 0, s);
+  if (cudaLaunchKernelEx(&l.cfg, k_copy_pages<N, DENSE>, p, list) != cudaSuccess) return -1;
   moe_prof_count(1);
   return 0;
 }

@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 4 : 3) k_qk_norm_rope(const
   using P = Piece<V>;
   using Raw = typename P::type;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
   const unsigned work = blockIdx.x * kWarpsPerCta + warp;   // below T + the warps of a full GPU: fits
   const unsigned t = work / (unsigned)split;
   if (t >= (unsigned)p.T) return;
@@ -348,8 +350,8 @@ template <typename T, int V> int launch_rope(const RopeParams &p, bool inter, bo
   const size_t smem = (size_t)kWarpsPerCta * (p.rot / 2) * sizeof(float2);
   const auto fn = inter ? (f8 ? k_qk_norm_rope<T, V, true, true> : k_qk_norm_rope<T, V, true, false>)
                         : (f8 ? k_qk_norm_rope<T, V, false, true> : k_qk_norm_rope<T, V, false, false>);
-  fn<<<grid, kThreads, smem, s>>>(p, lanes, split);
-  if (cudaGetLastError() != cudaSuccess) return -1;
+  PdlLaunch l(dim3(grid), kThreads, smem, s);
+  if (cudaLaunchKernelEx(&l.cfg, fn, p, lanes, split) != cudaSuccess) return -1;
   moe_prof_count(1);
   return 0;
 }
