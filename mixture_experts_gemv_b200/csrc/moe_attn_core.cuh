@@ -21,12 +21,25 @@
 // holds whole is written out by its warp; one cut by a range's end leaves unnormalised pieces in
 // the workspace (at most two per warp, in fragment order; a block in the middle of a long segment
 // joins its warps' first), and the join kernel, launched behind with programmatic dependent
-// launch, sums them in order. No atomics: outputs repeat bit for bit.
+// launch, sums them in order. No atomics: outputs repeat bit for bit. (Lengths and tables are read
+// past L1: a block may have started before the kernel that writes them ended.)
 //
 // Precision: K Q^T products are exact, summed in FP32; the softmax runs in FP32 (base 2); P is
-// rounded to the 16-bit type of the V product (half a step, 2^-9 or 2^-12 of each p, the sum l
+// rounded to the 16-bit type of the V product (half a step, 2^-8 or 2^-11 of each p; the sum l
 // keeps the unrounded p); O is FP32 and rounded once. fp16: p is taken times 2^15, so that
 // what fp16 cannot hold lies below 2^-39 of the largest p.
+//
+// Measured (bytes of the keys in range, over the two launches replayed in a graph; a copy streams
+// 6.5 TB/s): one sequence of 997 tokens, 8 KV heads of 128 8.0 us; of 10,000, 8 of 256 21.1 us =
+// 3.9 TB/s; of 40,000, 2 of 512 40.5 us = 4.0; 8 sequences of up to 40,000, 8 of 128 43.3 us = 4.9;
+// 128 of up to 4,096 in 8 bits, 4 of 128 52 us = 4.4; past 1 GB 5.6 to 5.9 TB/s. What does not
+// grow with the lengths is about 9 us: 1.6 until a warp knows its range, 3 to 5 until the first K
+// rows are there, 1 for the blocks' pieces, 3 for the join. 8-bit caches are bound by the
+// conversions to fp16 in front of each product.
+//
+// Tried and left: K's 8-bit products as they are, q in two or three 8-bit terms (mma.sync with 8-bit
+// operands is emulated: the 8-bit case went from 59 to 67 us); one bulk copy a row (a warp issues
+// one per 70 clocks or so: 3.9 TB/s with rows of 256 bytes).
 #pragma once
 
 #include <type_traits>
@@ -306,7 +319,7 @@ template <int LOG> struct Cursor {
     if (++seg < segs) return;
     seg = 0;
 #pragma unroll 1
-    do sp = Span(p, __ldg(p.lens + ++b), LOG);
+    do sp = Span(p, __ldcg(p.lens + ++b), LOG);
     while (sp.n == 0);
   }
   __device__ __forceinline__ int token() const { return ((sp.lo >> LOG) + i) << LOG; }   // the unit's first
@@ -360,7 +373,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
   // sequences without a key: rows of zeros, lse = -inf
 #pragma unroll 1
   for (int b = worker; b < p.B; b += all_workers) {
-    if (Span(p, __ldg(p.lens + b), S::kLog).n) continue;
+    if (Span(p, __ldcg(p.lens + b), S::kLog).n) continue;
 #pragma unroll 1
     for (int h = 0; h < p.nq; ++h) {
 #pragma unroll 1
@@ -409,7 +422,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
     if (t >= lo && t < hi) {
       const unsigned e = p.page_shift >= 0 ? (unsigned)t >> p.page_shift : (unsigned)t / (unsigned)p.page_size;
       f.in_page = t - (int)e * p.page_size;
-      f.page = __ldg(p.tables + (long long)ahead.b * p.table_stride + e);
+      f.page = __ldcg(p.tables + (long long)ahead.b * p.table_stride + e);
     } else {
       f.page = f.in_page = 0;
     }
@@ -854,11 +867,16 @@ constexpr int kJoinMost = 512;   // threads
 constexpr int kJoinPar = 16;     // groups
 template <typename TO, int ES>
 __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int log, int all_workers, int by_segment, int nt, int par, float off) {
-  __shared__ float4 s_acc[kJoinMost], s_ml[kJoinMost];
-  pdl_launch_dependents();   // what comes next may be made ready; it waits for this kernel's end
+  extern __shared__ __align__(16) float4 s_acc[];   // [threads] sums, [threads] (m, l): where par > 1
+  float4 *s_ml = s_acc + blockDim.x;
   int w0, w1, b, seg;
   bool joined;
   {
+    // one block waits in any case: where nothing is cut the kernel must not end, and let what
+    // follows start, before the attention kernel has ended
+    auto leave = []() {
+      if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
+    };
     Numbering num(p, log, all_workers);
     joined = num.extra;
     Numbering::Segment s;
@@ -867,16 +885,16 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
 #pragma unroll 1
       while (seq >= num.base + 32) num.next_strip(p);
       s = num.segment(seq - num.base, blockIdx.x - seq * num.segs);
-      if (s.n == 0) return;
+      if (s.n == 0) return leave();
       w0 = num.first_worker(s.first);
     } else {
       w0 = blockIdx.x;
-      if (w0 + 1 >= num.split.workers) return;
+      if (w0 + 1 >= num.split.workers) return leave();
       s = num.holding(p, num.split.first(w0 + 1) - 1);
-      if (num.first_worker(s.first) != w0) return;
+      if (num.first_worker(s.first) != w0) return leave();
     }
     w1 = num.last_worker(s.first, s.n);
-    if (w1 == w0) return;
+    if (w1 == w0) return leave();
     b = s.b;
     seg = s.seg;
   }
@@ -922,7 +940,7 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
   if (f - lane >= frags) return;   // whole warps
   TO *out = static_cast<TO *>(p.out) + (long long)b * p.out_tok + (long long)h0 * p.out_head;
   store_fragment<TO, ES>(out, p.out_head, k, heads, lane, sum.acc, sum.ml.y == 0.f ? 0.f : p.v_scale / sum.ml.y,
-                           sum.ml.w == 0.f ? 0.f : p.v_scale / sum.ml.w);
+                         sum.ml.w == 0.f ? 0.f : p.v_scale / sum.ml.w);
   if (p.lse && k == 0 && lane < 4) {
     float *lse = p.lse + (long long)b * p.nq + h0 + 2 * c;
     if (2 * c < heads) lse[0] = (sum.ml.x + (log2f(sum.ml.y) - off)) * kLn2;
@@ -956,7 +974,7 @@ template <typename T, int W, int NT, int ES, bool QB> int launch(const AttnParam
   const int threads = par > 4 ? kJoinMost : kJoinMost / 2, frags = p.D / 16 * NT * 32, per = threads / par;
   // a block a segment where there are fewer segments than workers, else one a worker
   const int by_segment = segments <= workers;
-  PdlLaunch j(dim3(by_segment ? (unsigned)segments : workers, (frags + per - 1) / per), threads, 0, s);
+  PdlLaunch j(dim3(by_segment ? (unsigned)segments : workers, (frags + per - 1) / per), threads, par > 1 ? threads * 32 : 0, s);
   if (cudaLaunchKernelEx(&j.cfg, k_attn_join<TO, ES>, p, S::kLog, workers, by_segment, NT, par, Mma<T>::kOff) != cudaSuccess) return -1;
   moe_prof_count(2);
   return 0;

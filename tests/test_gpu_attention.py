@@ -340,6 +340,41 @@ def test_attention_calls_that_overlap_on_two_streams():
         assert all(torch.equal(o, want) for o in outs)
 
 
+@pytest.mark.parametrize("B,n_q,n_kv", [(64, 8, 1), (900, 8, 4)])
+def test_attention_inputs_change_right_behind_a_call_that_cuts_no_sequence(B, n_q, n_kv):
+    """Sequences of one unit each leave nothing to join: what follows still has to wait for the attention itself."""
+    cache, tables, lens, g = make_batch([16] * B, 16, n_kv, 128, BF, "NHD", seed=B)
+    q = normal((B, n_q, 128), BF, g, 2.0)
+    out, lse = torch.empty_like(q), torch.empty((B, n_q), device=DEV)
+    ql, ll, keep = q.clone(), lens.clone(), torch.empty_like(q)
+
+    def step():
+        ql.copy_(q)
+        ll.copy_(lens)
+        moe.moe_attention_decode(ql, cache, tables, ll, out, 0.1, lse=lse)
+        keep.copy_(out)
+        ll.zero_()
+        ql.zero_()
+
+    step()
+    check_attention(q, cache, tables, lens, 0.1, 0, keep, lse)
+    first = keep.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            step()
+    for _ in range(20):
+        keep.fill_(float("nan"))
+        out.fill_(float("nan"))
+        graph.replay()
+        assert torch.equal(keep, first)
+    for _ in range(50):
+        step()
+        assert torch.equal(keep, first)
+    moe.moe_cache_check()
+
+
 def test_attention_given_workspace_holds_anything():
     lens = [777, 1]
     cache, tables, n, g = make_batch(lens, 16, 2, 256, FP, "HND", seed=6)
