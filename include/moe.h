@@ -312,19 +312,21 @@ typedef struct moe_heads {
  *   half layout: (a, b) = (i, i + rotary_dim / 2); interleaved: (2 i, 2 i + 1). Elements from
  *   rotary_dim on keep u.
  *   q, k, v     [T, n_q | n_kv, head_dim] of type dtype (MOE_DT_BF16 or MOE_DT_F16); n_q or n_kv
- *               may be 0; v is read only for the cache
+ *               may be 0, neither above 4096; v is read only for the cache
  *   positions   device int32 [T];  inv_freq device float64 [rotary_dim / 2]
  *   rotary_dim  0 (no rotation; positions and inv_freq may be NULL) to head_dim: a multiple of
  *               16 in the half layout, even when interleaved
  *   q_gain, k_gain  device fp32 [head_dim], 16-byte aligned, or NULL for no norm
  *   q_out, k_out    where rotated q and k go, type dtype; NULL leaves k_out out (q_out only
- *               where n_q = 0). Each may be its own input (same base and strides).
+ *               where n_q = 0). Each may be its own input (same base and strides), and none may
+ *               overlap anything else that the call reads or writes.
  *   cache, layer, slots  NULL, or the cache that k (rotated) and v are stored in: token t in row
  *               slots[t] % page_size of page slots[t] / page_size (device int64 [T]; negative:
  *               not stored). Its dtype is dtype or MOE_DT_E4M3 (value times 1 / scale in FP32, saturated at
  *               +-448). Slots that are not negative must be distinct: of tokens with the same
  *               slot, which one's values remain is not defined.
- * Sums and products in FP32, rounded once. T = 0 is a no-op.
+ * Sums and products in FP32, rounded once: with gains, a head whose squares or products with the
+ * gain pass FP32's range gives what FP32 gives. T = 0 is a no-op.
  */
 int moe_qk_norm_rope(const moe_heads *q, const moe_heads *k, const moe_heads *v, int dtype, int T, int n_q,
                      int n_kv, int head_dim, const int32_t *positions, const double *inv_freq, int rotary_dim,
@@ -361,10 +363,10 @@ int moe_rope_frequencies(int kind, int rotary_dim, double base, double factor, d
  *                i * page_size ... of a sequence. Entries past a sequence's end are not read.
  *   seq_lens     device int32 [B], keys per sequence. Length 0, and a sequence whose scores are
  *                all -inf, gives a row of zeros and lse = -inf.
- *   out          [B, n_q, head_dim] of q's type;  lse device fp32 [B, n_q] or NULL
+ *   out          [B, n_q, head_dim] of q's type, apart from q;  lse device fp32 [B, n_q] or NULL
  *   workspace    device, moe_attention_decode_workspace_bytes(...) bytes, 16-byte aligned; needs no
  *                initial contents and keeps nothing between calls
- * Limits: max_pages * page_size <= 2^30. Two launches on `stream`. Deterministic: the work split
+ * Limits: max_pages * page_size <= 2^30, n_q <= 4096. Two launches on `stream`. Deterministic: the work split
  * follows from the lengths alone and pieces are summed in order. Softmax in FP32; the
  * probabilities are rounded to 16 bits (bf16 for a bf16 cache, else fp16) for the product with v.
  */

@@ -130,14 +130,19 @@ bool same(const moe_heads *a, const moe_heads *b) {
   return a->p == b->p && a->token_stride == b->token_stride && a->head_stride == b->head_stride;
 }
 
-// Rows of T x n x D elements of 2 bytes as an address range.
-struct Range {
-  uintptr_t lo, hi;
-};
-Range range_of(const moe_heads *h, int T, int n, int D) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(h->p);
-  return {lo, lo + 2 * ((uintptr_t)(T - 1) * h->token_stride + (uintptr_t)(n - 1) * h->head_stride + D)};
+// Whether rows of T tokens of nx and of ny heads (2-byte elements) share an address.
+bool overlap(const moe_heads *x, int nx, const moe_heads *y, int ny, int T, int D) {
+  const long long wx = 2 * ((nx - 1) * x->head_stride + D), wy = 2 * ((ny - 1) * y->head_stride + D);   // a token's span
+  const uintptr_t ax = reinterpret_cast<uintptr_t>(x->p), ay = reinterpret_cast<uintptr_t>(y->p);
+  const uintptr_t bx = ax + 2 * (uintptr_t)(T - 1) * x->token_stride + wx, by = ay + 2 * (uintptr_t)(T - 1) * y->token_stride + wy;
+  if (ax >= by || ay >= bx) return false;
+  // parts of the rows of one buffer: apart when the spans are, modulo a token
+  if (x->token_stride != y->token_stride || x->token_stride == 0) return true;
+  const long long step = 2 * x->token_stride, gap = (((long long)(ay - ax)) % step + step) % step;
+  return gap < wx || gap + wy > step;
 }
+
+bool mult_of(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
 
@@ -158,6 +163,8 @@ int moe_qk_norm_rope(const moe_heads *q, const moe_heads *k, const moe_heads *v,
   if (rotary_dim && (!positions || !inv_freq)) return fail(MOE_ERR_BAD_ARG, "null pointer argument");
   if (!std::isfinite(rope_scale) || !(eps >= 0) || !std::isfinite(eps))
     return fail(MOE_ERR_BAD_ARG, "rope_scale must be finite, eps finite and not negative");
+  if (!mult_of(positions, 4) || !mult_of(inv_freq, 8) || !mult_of(slots, 8))
+    return fail(MOE_ERR_BAD_ALIGN, "positions, inv_freq and slots must be aligned to their elements");
   if (!mult16(q_gain) || !mult16(k_gain)) return fail(MOE_ERR_BAD_ALIGN, "q_gain and k_gain must be 16-byte aligned");
   const int rows = T > 0 ? T : 1;
   if (n_q) {
@@ -183,31 +190,20 @@ int moe_qk_norm_rope(const moe_heads *q, const moe_heads *k, const moe_heads *v,
     if (cache->n_kv != n_kv || cache->head_dim != head_dim)
       return fail(MOE_ERR_BAD_ARG, "the cache holds %d heads of %d, not %d of %d", cache->n_kv, cache->head_dim, n_kv, head_dim);
     if (!slots) return fail(MOE_ERR_BAD_ARG, "null pointer argument");
+    if (cache->k == cache->v) return fail(MOE_ERR_BAD_ARG, "k and v of the cache are the same tensor");
   }
   // an output may be its own input and must not touch another
-  {
-    struct Part { const char *name; const moe_heads *h; int n; bool out; } parts[] = {
-        {"q", n_q ? q : nullptr, n_q, false}, {"k", n_kv ? k : nullptr, n_kv, false},
-        {"v", cache ? v : nullptr, n_kv, false}, {"q_out", n_q ? q_out : nullptr, n_q, true}, {"k_out", k_out, n_kv, true}};
-    for (int o = 3; o < 5; ++o) {
-      if (!parts[o].h) continue;
-      const Range a = range_of(parts[o].h, rows, parts[o].n, head_dim);
-      for (int i = 0; i < 5; ++i) {
-        if (i == o || !parts[i].h || (i == o - 3 && same(parts[i].h, parts[o].h))) continue;
-        const Range b = range_of(parts[i].h, rows, parts[i].n, head_dim);
-        if (a.lo >= b.hi || b.lo >= a.hi) continue;
-        // parts of the rows of one buffer: apart when the heads' spans within a token are apart
-        const moe_heads *x = parts[o].h, *y = parts[i].h;
-        if (x->token_stride == y->token_stride && x->token_stride > 0) {
-          const long long step = 2 * x->token_stride;
-          const long long wx = 2 * ((parts[o].n - 1) * x->head_stride + head_dim), wy = 2 * ((parts[i].n - 1) * y->head_stride + head_dim);
-          const long long gap = ((long long)(b.lo - a.lo) % step + step) % step;   // y's start behind x's, modulo a token
-          if (gap >= wx && gap + wy <= step) continue;
-        }
-        return fail(MOE_ERR_BAD_ARG, "%s overlaps %s", parts[o].name, parts[i].name);
-      }
-    }
+  const struct { const char *name; const moe_heads *h; int n; } ins[] = {
+      {"q", n_q ? q : nullptr, n_q}, {"k", n_kv ? k : nullptr, n_kv}, {"v", cache ? v : nullptr, n_kv}};
+  const struct { const char *name; const moe_heads *h; int n; } outs[] = {{"q_out", n_q ? q_out : nullptr, n_q}, {"k_out", k_out, n_kv}};
+  for (int o = 0; o < 2; ++o) {
+    if (!outs[o].h) continue;
+    for (int i = 0; i < 3; ++i)
+      if (ins[i].h && !(i == o && same(ins[i].h, outs[o].h)) && overlap(outs[o].h, outs[o].n, ins[i].h, ins[i].n, rows, head_dim))
+        return fail(MOE_ERR_BAD_ARG, "%s overlaps %s", outs[o].name, ins[i].name);
   }
+  if (outs[0].h && outs[1].h && overlap(outs[0].h, n_q, outs[1].h, n_kv, rows, head_dim))
+    return fail(MOE_ERR_BAD_ARG, "q_out overlaps k_out");
   if (T == 0) return MOE_OK;
   Device *dev;
   rc = device(&dev);
@@ -292,7 +288,7 @@ static size_t attn_o_bytes(size_t rows, int D) { return 2ull * MOE_ATTN_MAX_WORK
 static size_t attn_ml_bytes(size_t rows) { return 2ull * MOE_ATTN_MAX_WORKERS * rows * 8; }
 
 size_t moe_attention_decode_workspace_bytes(int n_q, int n_kv, int head_dim) {
-  if (n_q < 1 || n_kv < 1 || n_q % n_kv || head_dim < 16 || head_dim > 512 || head_dim % 16) return 0;
+  if (n_q < 1 || n_q > 4096 || n_kv < 1 || n_q % n_kv || head_dim < 16 || head_dim > 512 || head_dim % 16) return 0;
   const size_t rows = attn_rows(n_q, n_kv, head_dim);
   return attn_o_bytes(rows, head_dim) + attn_ml_bytes(rows);
 }
@@ -317,10 +313,9 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
   const int D = cache->head_dim, rows_b = B > 0 ? B : 1;
   rc = check_apart(out, "out", rows_b, n_q, D);
   if (rc) return rc;
-  {
-    const Range a = range_of(out, rows_b, n_q, D), b = range_of(q, rows_b, n_q, D);
-    if (a.lo < b.hi && b.lo < a.hi) return fail(MOE_ERR_BAD_ARG, "out overlaps q");
-  }
+  if (overlap(out, n_q, q, n_q, rows_b, D)) return fail(MOE_ERR_BAD_ARG, "out overlaps q");
+  if (!mult_of(block_tables, 4) || !mult_of(seq_lens, 4) || !mult_of(lse, 4))
+    return fail(MOE_ERR_BAD_ALIGN, "block_tables, seq_lens and lse must be aligned to their elements");
   if (!mult16(workspace)) return fail(MOE_ERR_BAD_ALIGN, "workspace must be 16-byte aligned");
   const size_t need = moe_attention_decode_workspace_bytes(n_q, cache->n_kv, D);
   if (workspace_bytes < need) return fail(MOE_ERR_BAD_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -375,6 +370,7 @@ int moe_copy_pages(const moe_kv_cache *cache, const int32_t *src, const int32_t 
   if (rc) return rc;
   if (n < 0) return fail(MOE_ERR_BAD_ARG, "n = %d < 0", n);
   if (n && (!src || !dst)) return fail(MOE_ERR_BAD_ARG, "null pointer argument");
+  if (!mult_of(block_tables, 4)) return fail(MOE_ERR_BAD_ALIGN, "block_tables must be aligned to its elements");
   if (block_tables && (rows < 0 || cols < 0 || table_stride < cols))
     return fail(MOE_ERR_BAD_ARG, "block tables of %d x %d, rows %lld apart", rows, cols, table_stride);
   if (n > cache->num_pages) return fail(MOE_ERR_BAD_ARG, "%d copies into %d pages: a page is in dst twice", n, cache->num_pages);

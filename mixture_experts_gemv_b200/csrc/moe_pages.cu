@@ -7,6 +7,10 @@
 // 16-byte pieces a thread, all loads in flight before the stores. Sources and destinations are
 // disjoint (checked on the host), so the order of blocks does not matter. The table's blocks come
 // first in the grid and run beside the copies: each entry is looked up in the sorted sources.
+//
+// Measured (8 KV heads of 256, bf16, pages of 16): 601 pages of 5 layers and 32 rows of tables,
+// 788 MB moved, 120.0 us = 6.57 TB/s (a plain copy's rate); 8 pages of 30 layers, 63 MB, 11.1 us
+// = 5.7 TB/s, 1.5 us above the bytes: the launch and the first blocks' loads.
 #include "moe_attn.cuh"
 #include "moe_pages.cuh"
 
@@ -78,9 +82,7 @@ __global__ void __launch_bounds__(kThreads) k_copy_pages(const __grid_constant__
 template <int N, bool DENSE> int launch_part(CopyParams p, const int2 *pairs, cudaStream_t s) {
   Pairs<N> list;
   for (int i = 0; i < p.n; ++i) list.v[i] = pairs[i];
-  p.stretches = (int)((p.pieces + kThreads * kPer - 1) / (kThreads * kPer));
   const long long blocks = p.table_blocks + (long long)p.stretches * p.n * p.layers * 2;
-  if (blocks > 0x7fffffffll) return -2;
   PdlLaunch l(dim3((unsigned)blocks), kThreads, 0, s);
   if (cudaLaunchKernelEx(&l.cfg, k_copy_pages<N, DENSE>, p, list) != cudaSuccess) return -1;
   moe_prof_count(1);
@@ -96,6 +98,9 @@ int moe_launch_copy_pages(CopyParams p, const int2 *pairs, int n, cudaStream_t s
     const long long want = ((long long)p.rows * p.cols + kThreads - 1) / kThreads;
     p.table_blocks = (int)(want < 592 ? want : 592);   // up to four blocks an SM
   }
+  const long long stretches = (p.pieces + kThreads * kPer - 1) / (kThreads * kPer);
+  if (p.table_blocks + (double)stretches * (n < kManyPairs ? n : kManyPairs) * p.layers * 2 > 2147483647.0) return -2;
+  p.stretches = (int)stretches;
   // lists above the parameter limit run as several launches: the pairs are independent of each
   // other, and no destination is another pair's source, so a table entry moves once
   for (int i = 0; i < n; i += kManyPairs) {

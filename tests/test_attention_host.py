@@ -80,8 +80,15 @@ def test_attention_refusals(L):
     for a in (dict(q=heads(FAKE + 2)), dict(q=heads(head=68)), dict(out=heads(FAKE * 8, 516)), dict(ws=FAKE + 8)):
         assert attn(L, **a) == -3, a
     assert attn(L, B=0) == 0
+    for a in (dict(tables=FAKE + 2), dict(lens=FAKE + 1)):
+        assert attn(L, **a) == -3, a
+    # out may lie between q's heads and tokens of one buffer, not on them
+    assert attn(L, B=0, q=heads(FAKE, 1024, 64), out=heads(FAKE + 512, 1024, 64)) == 0
+    assert attn(L, B=3, q=heads(FAKE, 1024, 64), out=heads(FAKE + 504 + 4, 1024, 64)) == -3
+    assert attn(L, B=3, q=heads(FAKE, 1024, 64), out=heads(FAKE + 496, 1024, 64)) == -2
     assert L.moe_attention_decode_workspace_bytes(5, 2, 64) == 0
     assert L.moe_attention_decode_workspace_bytes(4, 2, 65) == 0
+    assert L.moe_attention_decode_workspace_bytes(8192, 2, 64) == 0
     assert L.moe_attention_decode_workspace_bytes(4, 0, 64) == 0
 
 
@@ -102,7 +109,8 @@ def test_norm_rope_refusals(L):
               dict(qo=heads(FAKE * 7, 128, 64)), dict(qo=heads(FAKE, 512, 128)), dict(qo=heads(FAKE + 128)), dict(ko=heads(FAKE * 7)),
               dict(qo=heads(FAKE * 3)), dict(c=c, qo=heads(FAKE * 5)), dict(qo=heads(FAKE * 3 - 256))):
         assert rope(L, **a) == -2, a
-    for a in (dict(q=heads(FAKE + 8)), dict(qg=FAKE + 4), dict(kg=FAKE + 8), dict(ko=heads(FAKE * 9, 516)), dict(c=kv(v=FAKE + 2))):
+    assert rope(L, c=kv(k=FAKE * 64, v=FAKE * 64)) == -2
+    for a in (dict(q=heads(FAKE + 8)), dict(pos=FAKE + 2), dict(inv=FAKE + 4), dict(c=c, slots=FAKE + 4), dict(qg=FAKE + 4), dict(kg=FAKE + 8), dict(ko=heads(FAKE * 9, 516)), dict(c=kv(v=FAKE + 2))):
         assert rope(L, **a) == -3, a
     assert rope(L, T=0) == 0
     # q and k as parts of one buffer's rows may be turned in place; a part that reaches into the next may not
@@ -123,12 +131,22 @@ def test_copy_pages_refusals(L):
                      (list(range(50)) + [0], [49] * 51)):
         code(L, pages(L, src, dst), -2, "page" if len(src) < 50 else "pages")
     code(L, pages(L, [1, 1], [2, 3], tables=FAKE), -2, "moves twice")
+    code(L, pages(L, [1], [2], tables=FAKE + 2), -3)
     code(L, pages(L, [1], [2], tables=FAKE, stride=3), -2)
     code(L, pages(L, [1], [2], tables=FAKE, rows=-1), -2)
     assert pages(L, [], []) == 0
     assert L.moe_copy_pages(kv(), None, None, 1, None, 0, 0, 0, None) == -2
     assert L.moe_copy_pages(kv(), None, None, -1, None, 0, 0, 0, None) == -2
     assert L.moe_copy_pages(None, None, None, 0, None, 0, 0, 0, None) == -2
+
+
+def test_good_calls_without_a_gpu_fail_cleanly(L):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert attn(L) in (-4, -6)
+    assert rope(L) in (-4, -6)
+    assert pages(L, [1], [2]) in (-4, -6)
+    assert L.moe_cache_check(None) in (-4, -6)
 
 
 def test_binding_refuses_what_the_library_cannot_see():
