@@ -127,7 +127,7 @@ class PagedKvCache:
             plan.append((row, have, n, fresh, shared))
         if need > len(self._free):
             _refuse(f"append: {need} pages needed, {len(self._free)} free")
-        src, dst, tables, lens, positions, slots = [], [], {}, {}, [], []
+        src, dst, tables, lens, parts = [], [], {}, {}, []
         for row, have, n, fresh, shared in plan:
             pages = self._rows[row]
             if shared:
@@ -142,13 +142,14 @@ class PagedKvCache:
                 tables[row, len(pages) - 1] = pages[-1]
             if n:
                 self._len[row] = lens[row] = have + n
-            for t in range(have, have + n):
-                positions.append(t)
-                slots.append(pages[t // self.page_size] * self.page_size + t % self.page_size)
+            t = torch.arange(have, have + n)
+            first = have // self.page_size
+            page = torch.tensor(pages[first:], dtype=torch.int64)[t // self.page_size - first] if n else t
+            parts.append(torch.stack((t, page * self.page_size + t % self.page_size)))
         if src:
             self.ops.copy_pages(self.cache, src, dst)
         self._upload(tables, lens)
-        host = torch.tensor([positions, slots], dtype=torch.int64)
+        host = torch.cat(parts, dim=1) if parts else torch.empty((2, 0), dtype=torch.int64)
         if self.device.type == "cuda":
             host = host.pin_memory()
         dev = host.to(self.device, non_blocking=True)
