@@ -366,7 +366,7 @@ int moe_rope_frequencies(int kind, int rotary_dim, double base, double factor, d
  *   out          [B, n_q, head_dim] of q's type, apart from q;  lse device fp32 [B, n_q] or NULL
  *   workspace    device, moe_attention_decode_workspace_bytes(...) bytes, 16-byte aligned; needs no
  *                initial contents and keeps nothing between calls
- * Limits: max_pages * page_size <= 2^30, n_q <= 4096. Two launches on `stream`. Deterministic: the work split
+ * Limits: max_pages * page_size <= 2^30, B <= 2^30, n_q <= 4096. Two launches on `stream`. Deterministic: the work split
  * follows from the lengths alone and pieces are summed in order. Softmax in FP32; the
  * probabilities are rounded to 16 bits (bf16 for a bf16 cache, else fp16) for the product with v.
  */

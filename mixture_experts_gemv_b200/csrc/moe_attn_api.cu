@@ -282,7 +282,7 @@ int moe_rope_frequencies(int kind, int rotary_dim, double base, double factor, d
   return MOE_OK;
 }
 
-// Layout of the workspace: partial sums, then (maximum, sum) pairs.
+// Layout of the workspace: partial sums, (maximum, sum) pairs, records of cut segments.
 static size_t attn_rows(int n_q, int n_kv, int D) { return 8 * (size_t)moe_attn_tiles(D, n_q / n_kv); }
 static size_t attn_o_bytes(size_t rows, int D) { return 2ull * MOE_ATTN_MAX_WORKERS * rows * D * 4; }
 static size_t attn_ml_bytes(size_t rows) { return 2ull * MOE_ATTN_MAX_WORKERS * rows * 8; }
@@ -290,7 +290,7 @@ static size_t attn_ml_bytes(size_t rows) { return 2ull * MOE_ATTN_MAX_WORKERS * 
 size_t moe_attention_decode_workspace_bytes(int n_q, int n_kv, int head_dim) {
   if (n_q < 1 || n_q > 4096 || n_kv < 1 || n_q % n_kv || head_dim < 16 || head_dim > 512 || head_dim % 16) return 0;
   const size_t rows = attn_rows(n_q, n_kv, head_dim);
-  return attn_o_bytes(rows, head_dim) + attn_ml_bytes(rows);
+  return attn_o_bytes(rows, head_dim) + attn_ml_bytes(rows) + MOE_ATTN_MAX_WORKERS * sizeof(int4);
 }
 
 int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cache, int layer, const int32_t *block_tables,
@@ -303,7 +303,7 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
   if (!rc) rc = check_heads(q, "q");
   if (!rc) rc = check_heads(out, "out");
   if (rc) return rc;
-  if (B < 0 || n_q < 1 || n_q % cache->n_kv || n_q > 4096)
+  if (B < 0 || B > (1 << 30) || n_q < 1 || n_q % cache->n_kv || n_q > 4096)
     return fail(MOE_ERR_BAD_ARG, "bad shape B = %d, n_q = %d over n_kv = %d", B, n_q, cache->n_kv);
   if (max_pages < 1 || table_stride < max_pages || (long long)max_pages * cache->page_size > (1ll << 30))
     return fail(MOE_ERR_BAD_ARG, "max_pages = %d (rows %lld apart) of %d tokens: need 1 <= max_pages <= table_stride and at "
@@ -354,6 +354,7 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
   char *ws = static_cast<char *>(workspace);
   p.ws_o = reinterpret_cast<float *>(ws);
   p.ws_ml = reinterpret_cast<float2 *>(ws + attn_o_bytes(rows, D));
+  p.ws_cut = reinterpret_cast<int4 *>(ws + attn_o_bytes(rows, D) + attn_ml_bytes(rows));
   p.err = dev->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   rc = cache->dtype == MOE_DT_E4M3 ? moe_launch_attn_e4m3(p, dev->num_sms, dtype == MOE_DT_BF16, s)

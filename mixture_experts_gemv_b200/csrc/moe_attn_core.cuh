@@ -21,8 +21,7 @@
 // holds whole is written out by its warp; one cut by a range's end leaves unnormalised pieces in
 // the workspace (at most two per warp, in fragment order; a block in the middle of a long segment
 // joins its warps' first), and the join kernel, launched behind with programmatic dependent
-// launch, sums them in order. No atomics: outputs repeat bit for bit. (Lengths and tables are read
-// past L1: a block may have started before the kernel that writes them ended.)
+// launch, sums them in order. No atomics: outputs repeat bit for bit.
 //
 // Precision: K Q^T products are exact, summed in FP32; the softmax runs in FP32 (base 2); P is
 // rounded to the 16-bit type of the V product (half a step, 2^-8 or 2^-11 of each p; the sum l
@@ -30,12 +29,13 @@
 // what fp16 cannot hold lies below 2^-39 of the largest p.
 //
 // Measured (bytes of the keys in range, over the two launches replayed in a graph; a copy streams
-// 6.5 TB/s): one sequence of 997 tokens, 8 KV heads of 128 8.0 us; of 10,000, 8 of 256 21.1 us =
-// 3.9 TB/s; of 40,000, 2 of 512 40.5 us = 4.0; 8 sequences of up to 40,000, 8 of 128 43.3 us = 4.9;
-// 128 of up to 4,096 in 8 bits, 4 of 128 52 us = 4.4; past 1 GB 5.6 to 5.9 TB/s. What does not
+// 6.5 TB/s): one sequence of 997 tokens, 8 KV heads of 128 8.4 us; of 10,000, 8 of 256 21.9 us =
+// 3.7 TB/s; of 40,000, 2 of 512 41.6 us = 3.9; 8 sequences of up to 40,000, 8 of 128 43.3 us = 4.9;
+// 128 of up to 4,096 in 8 bits, 4 of 128 48 us = 4.7; past 1 GB 5.6 to 5.9 TB/s. What does not
 // grow with the lengths is about 9 us: 1.6 until a warp knows its range, 3 to 5 until the first K
-// rows are there, 1 for the blocks' pieces, 3 for the join. 8-bit caches are bound by the
-// conversions to fp16 in front of each product.
+// rows are there, 1 for the blocks' pieces, 3 for the join; and 0.01 us a sequence, for the
+// numbering: 1,024 sequences of 64 tokens of one KV head take 15 us. 8-bit caches are bound by
+// instructions, the conversions to fp16 among them.
 //
 // Tried and left: K's 8-bit products as they are, q in two or three 8-bit terms (mma.sync with 8-bit
 // operands is emulated: the 8-bit case went from 59 to 67 us); one bulk copy a row (a warp issues
@@ -134,16 +134,12 @@ template <int W, int NT, int ES> struct Shape {
 };
 
 // Keys [lo, len) of a sequence: n units of 2^LOG tokens from unit number lo >> LOG on. A bad length is
-// cut to what the table can hold.
+// cut to [0, what the table can hold] (Numbering reports it).
 struct Span {
   int len, lo, n;
   __device__ __forceinline__ Span() : len(0), lo(0), n(0) {}
   __device__ __forceinline__ Span(const AttnParams &p, int length, int log) {
-    if ((unsigned)length > (unsigned)p.max_tokens) {
-      atomicCAS(p.err, 0u, MOE_DEV_ERR_BAD_LENGTH);
-      length = length < 0 ? 0 : p.max_tokens;
-    }
-    len = length;
+    len = min(max(length, 0), p.max_tokens);
     lo = p.window > 0 && len > p.window ? len - p.window : 0;
     n = len > 0 ? ((len - 1) >> log) + 1 - (lo >> log) : 0;
   }
@@ -218,50 +214,80 @@ struct Joined {
 // where workers have several, one more that comes first: its q, its ends and its result (eight
 // one-unit segments in one warp's range took 5 to 8 us beside a 36 us stream of 40,000 tokens).
 // Every worker's range of costs still holds a unit: no two of the extra ones are neighbours.
-// Held by a warp: lane l has sequence base + l of the strip of 32 that was looked at last.
-struct Numbering {
+// Held by a warp: lane l has sequences base + 4 l .. of the strip that was looked at last.
+// COLD: lengths are read past L1.
+template <bool COLD> struct Numbering {
   static constexpr unsigned kAll = 0xffffffffu;
+  static constexpr int kOwn = 4, kStrip = 32 * kOwn;
   int segs, extra, log;
   long long units;      // of all sequences, for one segment each
   Split split;
   int base;             // the strip, and what comes before it
   long long before;     // units
   int before_filled;    // sequences with a key
-  int n, filled;        // the lane's units, and sequences with a key up to it
-  long long inc;        // units up to the lane's sequence, inclusive
-  int len;              // the lane's length
+  int n[kOwn], len[kOwn];   // the lane's units and lengths
+  long long inc;        // units up to the lane's last sequence, inclusive
+  int filled;           // sequences with a key up to there
+  int next[kOwn];       // the next strip's lengths
 
-  __device__ __forceinline__ void strip(const AttnParams &p, int at) {
+  __device__ __forceinline__ void load(const AttnParams &p, int at, int (&to)[kOwn]) const {
+    const int b = at + kOwn * (threadIdx.x & 31);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      to[j] = 0;
+      if (b + j < p.B) to[j] = COLD ? __ldcg(p.lens + b + j) : p.lens[b + j];
+    }
+  }
+  __device__ __forceinline__ void strip(const AttnParams &p, int at) {   // `next` holds its lengths
     const int lane = threadIdx.x & 31;
     base = at;
-    len = base + lane < p.B ? __ldcg(p.lens + base + lane) : 0;
-    n = Span(p, len, log).n;
-    unsigned sum = n;   // of 32 lengths below 2^30 over 16: fits
+    unsigned sum = 0, keyed = 0;   // a lane's sum: four lengths up to 2^30 over 16
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      len[j] = next[j];
+      n[j] = Span(p, len[j], log).n;
+      sum += n[j];
+      keyed += n[j] > 0;
+    }
+    load(p, at + kStrip, next);
+    // both in one scan: the strip's units stay below 2^34
+    unsigned long long both = (unsigned long long)keyed << 40 | sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned t = __shfl_up_sync(kAll, sum, o);
-      if (lane >= o) sum += t;
+      const unsigned long long t = __shfl_up_sync(kAll, both, o);
+      if (lane >= o) both += t;
     }
-    inc = before + sum;
-    filled = before_filled + __popc(__ballot_sync(kAll, n > 0) & (kAll >> (31 - lane)));
+    inc = before + (long long)(both & ((1ull << 40) - 1));
+    filled = before_filled + (int)(both >> 40);
   }
   __device__ __forceinline__ void next_strip(const AttnParams &p) {
     before = __shfl_sync(kAll, inc, 31);
     before_filled = __shfl_sync(kAll, filled, 31);
-    strip(p, base + 32);
+    strip(p, base + kStrip);
   }
   __device__ __forceinline__ Numbering(const AttnParams &p, int log_, int all_workers) : segs(p.nkv * p.n_groups), extra(0), log(log_), before(0), before_filled(0) {
+    load(p, 0, next);
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) bad |= (unsigned)next[j] > (unsigned)p.max_tokens;
     strip(p, 0);
     units = __shfl_sync(kAll, inc, 31);
     int with_key = __shfl_sync(kAll, filled, 31);
-    if (p.B > 32) {
+    if (p.B > kStrip) {
       long long more = 0;
       int more_keys = 0;
 #pragma unroll 1
-      for (int b = 32 + (threadIdx.x & 31); b < p.B; b += 32) {
-        const int m = Span(p, __ldcg(p.lens + b), log).n;
-        more += m;
-        more_keys += m > 0;
+      for (int at = kStrip; at < p.B; at += 2 * kStrip) {
+        int x[kOwn], y[kOwn];
+        load(p, at, x);
+        load(p, at + kStrip, y);   // zeros past the last sequence
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+          const int m = Span(p, x[j], log).n, m2 = Span(p, y[j], log).n;
+          more += m + (long long)m2;
+          more_keys += (m > 0) + (m2 > 0);
+          bad |= (unsigned)x[j] > (unsigned)p.max_tokens || (unsigned)y[j] > (unsigned)p.max_tokens;
+        }
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
@@ -271,6 +297,7 @@ struct Numbering {
       units += more;
       with_key += more_keys;
     }
+    if (!COLD && bad) atomicCAS(p.err, 0u, MOE_DEV_ERR_BAD_LENGTH);
     extra = (units + with_key) * segs >= 2ll * all_workers ? 1 : 0;
     split = Split((units + extra * with_key) * segs, all_workers);
   }
@@ -281,13 +308,20 @@ struct Numbering {
     long long units_before;   // units of all segments before it
   };
   __device__ __forceinline__ Segment segment(int src, int seg) const {   // of the strip's sequence src
+    const int lane = src / kOwn, own = src % kOwn;
+    int n_ = n[0], len_ = len[0], behind = 0, behind_keyed = 0;   // sequence `own` of the lane, and what follows it there
+#pragma unroll
+    for (int j = 1; j < kOwn; ++j) {
+      if (own == j) n_ = n[j], len_ = len[j];
+      if (own < j) behind += n[j], behind_keyed += n[j] > 0;
+    }
     Segment s;
     s.b = base + src;
     s.seg = seg;
-    s.n = __shfl_sync(kAll, n, src);
-    s.len = __shfl_sync(kAll, len, src);
-    const long long u = __shfl_sync(kAll, inc, src) - s.n;
-    const int f = __shfl_sync(kAll, filled, src) - 1;
+    s.n = __shfl_sync(kAll, n_, lane);
+    s.len = __shfl_sync(kAll, len_, lane);
+    const long long u = __shfl_sync(kAll, inc - behind - n_, lane);
+    const int f = __shfl_sync(kAll, filled - behind_keyed, lane) - 1;
     s.first = (u + extra * f) * segs + (long long)seg * (s.n + extra);
     s.units_before = u * segs + (long long)seg * s.n;
     return s;
@@ -297,16 +331,22 @@ struct Numbering {
     unsigned hit;
 #pragma unroll 1
     while (!(hit = __ballot_sync(kAll, cost < (inc + extra * filled) * segs))) next_strip(p);
-    const int src = __ffs(hit) - 1;
-    Segment s = segment(src, 0);
+    const int lane = __ffs(hit) - 1;
+    // the first of the lane's sequences that ends behind the cost
+    int own = 0, behind = 0, behind_keyed = 0;
+#pragma unroll
+    for (int j = kOwn - 1; j > 0; --j) {
+      behind += n[j];
+      behind_keyed += n[j] > 0;
+      if (own == 0 && cost >= (inc - behind + extra * (filled - behind_keyed)) * segs) own = j;
+    }
+    Segment s = segment(lane * kOwn + __shfl_sync(kAll, own, lane), 0);
     s.seg = (int)quotient(cost - s.first, s.n + extra);
     s.first += (long long)s.seg * (s.n + extra);
     s.units_before += (long long)s.seg * s.n;
     return s;
   }
   __device__ __forceinline__ int unit(const Segment &s, long long cost) const { return max((int)(cost - s.first) - extra, 0); }
-  __device__ __forceinline__ int first_worker(long long first) const { return split.owner(first + extra); }
-  __device__ __forceinline__ int last_worker(long long first, int n_) const { return split.owner(first + extra + n_ - 1); }
 };
 
 // A place in the numbering: unit i of segment seg of sequence b.
@@ -319,7 +359,7 @@ template <int LOG> struct Cursor {
     if (++seg < segs) return;
     seg = 0;
 #pragma unroll 1
-    do sp = Span(p, __ldcg(p.lens + ++b), LOG);
+    do sp = Span(p, p.lens[++b], LOG);
     while (sp.n == 0);
   }
   __device__ __forceinline__ int token() const { return ((sp.lo >> LOG) + i) << LOG; }   // the unit's first
@@ -365,7 +405,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
 
   // ---- the warp's range of units
   const int all_workers = kWarps * gridDim.x;
-  Numbering num(p, S::kLog, all_workers);
+  Numbering<false> num(p, S::kLog, all_workers);
   const int segs = num.segs, workers = num.split.workers;
   // Neighbours in the numbering are on different SMs where there is little to do, else in one
   // block, which can then join its warps' pieces
@@ -373,33 +413,42 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
   // sequences without a key: rows of zeros, lse = -inf
 #pragma unroll 1
   for (int b = worker; b < p.B; b += all_workers) {
-    if (Span(p, __ldcg(p.lens + b), S::kLog).n) continue;
+    if (Span(p, p.lens[b], S::kLog).n) continue;
 #pragma unroll 1
     for (int h = 0; h < p.nq; ++h) {
 #pragma unroll 1
       for (int d = lane; d < p.D; d += 32) static_cast<TO *>(p.out)[(long long)b * p.out_tok + (long long)h * p.out_head + d] = TO(0.f);
       if (p.lse && lane == 0) p.lse[(long long)b * p.nq + h] = ninf;
     }
+    if (p.noted && p.by_segment) {   // nothing to join
+#pragma unroll 1
+      for (int x = lane; x < segs; x += 32) p.ws_cut[b * segs + x] = make_int4(0, 0, 0, 0);
+    }
   }
+  if (p.noted && !p.by_segment && lane == 0) p.ws_cut[worker] = make_int4(0, 0, 0, 0);   // for now
   if (worker >= workers) return;
   Cursor<S::kLog> at;        // the unit that is computed next
   long long seg_first;       // first cost of its segment
   int count;                 // the warp's units
   {
-    const long long from = num.split.first(worker), to = num.split.first(worker + 1);
-    const Numbering::Segment s = num.holding(p, from);
-    at.b = s.b;
-    at.seg = s.seg;
-    at.i = num.unit(s, from);
-    at.sp = Span(p, s.len, S::kLog);
-    seg_first = s.first;
-    const long long begin = s.units_before + at.i;
-    if (worker + 1 == workers) {
-      count = (int)(num.units * segs - begin);
-    } else {
-      const Numbering::Segment e = num.holding(p, to);
-      count = (int)(e.units_before + num.unit(e, to) - begin);
+    long long begin = 0, end = num.units * segs;   // in units
+#pragma unroll 1
+    for (int x = 0; x < 2 && worker + x < workers; ++x) {   // where the range starts and where the next one does
+      const long long cost = num.split.first(worker + x);
+      const auto s = num.holding(p, cost);
+      const int i = num.unit(s, cost);
+      if (x == 0) {
+        at.b = s.b;
+        at.seg = s.seg;
+        at.i = i;
+        at.sp = Span(p, s.len, S::kLog);
+        seg_first = s.first;
+        begin = s.units_before + i;
+      } else {
+        end = s.units_before + i;
+      }
     }
+    count = (int)(end - begin);
   }
   const Split split = num.split;
   const int extra = num.extra;
@@ -538,9 +587,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
     const int heads = min(S::kRows, (kvh + 1) * p.group - h0);
     const int i0 = at.i, cnt = min(at.sp.n - i0, count - done);
     const bool whole = cnt == at.sp.n;
-    // whether the block's four warps have nothing but parts of this segment
-    const bool in_block = !whole && extra &&
-                          Block(blockIdx.x).inside(split.owner(seg_first + extra), split.owner(seg_first + extra + at.sp.n - 1));
+    bool in_block = false;   // whether the block's four warps have nothing but parts of this segment
+    if (!whole && (extra || p.noted)) {
+      const int w0 = split.owner(seg_first + extra), w1 = split.owner(seg_first + extra + at.sp.n - 1);
+      in_block = extra && Block(blockIdx.x).inside(w0, w1);
+      if (p.noted && i0 == 0 && lane == 0) p.ws_cut[p.by_segment ? at.b * segs + at.seg : worker] = make_int4(w0 | extra << 16, w1, at.b, at.seg);
+    } else if (whole && p.noted && p.by_segment && lane == 0) {
+      p.ws_cut[at.b * segs + at.seg] = make_int4(0, 0, 0, 0);
+    }
 
     uint32_t qf[W / 16][NT][2];
     float sc[NT][2];   // score scale of the lane's two columns
@@ -858,45 +912,49 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
 }
 
 // Sums the pieces of one cut segment: segment blockIdx.x (by_segment), or the one that starts in
-// worker blockIdx.x and goes on behind it. Which workers have its pieces follows from the lengths,
-// before the attention kernel's results are waited for (that kernel lets this one start only when
-// what came before it is done, so the lengths are there). A thread takes one fragment of a piece
-// (two heads at two elements: four values), of every par-th piece: the block's threads are par
-// groups over the same threads / par fragments. Then the groups' sums are joined.
+// worker blockIdx.x and goes on behind it. NOTED: which workers have its pieces is what the worker
+// that starts it noted. Otherwise (few segments, by_segment) it follows from the lengths, before the
+// attention kernel's results are waited for: that kernel lets this one start only when what came
+// before it is done, so the lengths are there; they are read past L1. (Noted, calls of up to eight
+// sequences took 0.3 to 1.7 us more; numbered here, 128 sequences of 4 KV heads took 4 us more and
+// 1,024 short ones 12.) A thread takes one fragment of a piece (two heads at two elements: four values), of every par-th
+// piece: the block's threads are par groups over the same threads / par fragments. Then the
+// groups' sums are joined.
 constexpr int kJoinMost = 512;   // threads
 constexpr int kJoinPar = 16;     // groups
-template <typename TO, int ES>
-__global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int log, int all_workers, int by_segment, int nt, int par, float off) {
+template <typename TO, int ES, bool NOTED>
+__global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int log, int all_workers, int nt, int par, float off) {
   extern __shared__ __align__(16) float4 s_acc[];   // [threads] sums, [threads] (m, l): where par > 1
   float4 *s_ml = s_acc + blockDim.x;
   int w0, w1, b, seg;
   bool joined;
-  {
-    // one block waits in any case: where nothing is cut the kernel must not end, and let what
-    // follows start, before the attention kernel has ended
-    auto leave = []() {
-      if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
-    };
-    Numbering num(p, log, all_workers);
-    joined = num.extra;
-    Numbering::Segment s;
-    if (by_segment) {
-      const int seq = blockIdx.x / num.segs;
+  if constexpr (NOTED) {
+    pdl_wait();
+    const int4 cut = __ldcg(p.ws_cut + blockIdx.x);
+    w0 = cut.x & 0xffff;
+    w1 = cut.y;
+    b = cut.z;
+    seg = cut.w;
+    joined = cut.x >> 16;
+  } else {
+    Numbering<true> num(p, log, all_workers);
+    b = blockIdx.x / num.segs;
+    seg = blockIdx.x - b * num.segs;
 #pragma unroll 1
-      while (seq >= num.base + 32) num.next_strip(p);
-      s = num.segment(seq - num.base, blockIdx.x - seq * num.segs);
-      if (s.n == 0) return leave();
-      w0 = num.first_worker(s.first);
-    } else {
-      w0 = blockIdx.x;
-      if (w0 + 1 >= num.split.workers) return leave();
-      s = num.holding(p, num.split.first(w0 + 1) - 1);
-      if (num.first_worker(s.first) != w0) return leave();
+    while (b >= num.base + num.kStrip) num.next_strip(p);
+    const Numbering<true>::Segment s = num.segment(b - num.base, seg);
+    w0 = w1 = 0;
+    if (s.n) {
+      w0 = num.split.owner(s.first + num.extra);
+      w1 = num.split.owner(s.first + num.extra + s.n - 1);
     }
-    w1 = num.last_worker(s.first, s.n);
-    if (w1 == w0) return leave();
-    b = s.b;
-    seg = s.seg;
+    joined = num.extra;
+  }
+  if (w1 == w0) {
+    // nothing to join. One block waits all the same: this kernel must not end, and let what follows
+    // start, before the attention kernel has ended
+    if (!NOTED && blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
+    return;
   }
   const int tid = threadIdx.x, lane = tid & 31, per = blockDim.x / par, j0 = tid / per;   // per: a multiple of 32
   const int frags = p.D / 16 * nt * 32, f = blockIdx.y * per + (tid - j0 * per);
@@ -905,7 +963,7 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
   const int heads = (kvh + 1) * p.group - h0;   // that exist from this column tile on
   const Pieces pieces(w0, w1, joined);
   const float4 *po = reinterpret_cast<const float4 *>(p.ws_o) + f, *pm = reinterpret_cast<const float4 *>(p.ws_ml) + (4 * n + c);
-  pdl_wait();
+  if (!NOTED) pdl_wait();
   Joined sum;
   if (f < frags) {
     constexpr int kAhead = 4;
@@ -948,7 +1006,7 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
   }
 }
 
-template <typename T, int W, int NT, int ES, bool QB> int launch(const AttnParams &p, int num_sms, cudaStream_t s) {
+template <typename T, int W, int NT, int ES, bool QB> int launch(AttnParams p, int num_sms, cudaStream_t s) {
   using S = Shape<W, NT, ES>;
   using TO = std::conditional_t<ES == 1 && QB, __nv_bfloat16, T>;
   static unsigned long long attr_done = 0;
@@ -964,18 +1022,18 @@ template <typename T, int W, int NT, int ES, bool QB> int launch(const AttnParam
   if (grid * kWarps > MOE_ATTN_MAX_WORKERS) grid = MOE_ATTN_MAX_WORKERS / kWarps;
   const long long segments = (long long)p.B * p.nkv * p.n_groups;
   const int workers = grid * kWarps;
-  PdlLaunch l(dim3(grid), kWarps * 32, S::kSmem, s);
-  if (cudaLaunchKernelEx(&l.cfg, fn, p) != cudaSuccess) return -1;
+  p.by_segment = segments <= workers;   // a block of the join a segment, or one a worker
   // Threads that share a fragment in the join: as many as a quarter of the pieces that a segment
   // has when all are equally long and blocks join theirs, so that each one's loads are in flight
   // together
   int par = 1;
   while (par < kJoinPar && 4 * par * segments < grid) par *= 2;
+  p.noted = par == 1;   // few segments: the join finds their workers itself
+  PdlLaunch l(dim3(grid), kWarps * 32, S::kSmem, s);
+  if (cudaLaunchKernelEx(&l.cfg, fn, p) != cudaSuccess) return -1;
   const int threads = par > 4 ? kJoinMost : kJoinMost / 2, frags = p.D / 16 * NT * 32, per = threads / par;
-  // a block a segment where there are fewer segments than workers, else one a worker
-  const int by_segment = segments <= workers;
-  PdlLaunch j(dim3(by_segment ? (unsigned)segments : workers, (frags + per - 1) / per), threads, par > 1 ? threads * 32 : 0, s);
-  if (cudaLaunchKernelEx(&j.cfg, k_attn_join<TO, ES>, p, S::kLog, workers, by_segment, NT, par, Mma<T>::kOff) != cudaSuccess) return -1;
+  PdlLaunch j(dim3(p.by_segment ? (unsigned)segments : workers, (frags + per - 1) / per), threads, par > 1 ? threads * 32 : 0, s);
+  if (cudaLaunchKernelEx(&j.cfg, p.noted ? k_attn_join<TO, ES, true> : k_attn_join<TO, ES, false>, p, S::kLog, workers, NT, par, Mma<T>::kOff) != cudaSuccess) return -1;
   moe_prof_count(2);
   return 0;
 }

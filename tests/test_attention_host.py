@@ -72,7 +72,7 @@ def attn(L, q=None, dt=0, c=None, layer=0, tables=FAKE, stride=4, cols=4, lens=F
 
 def test_attention_refusals(L):
     for a in (dict(dt=2), dict(dt=7), dict(dt=1), dict(layer=2), dict(layer=-1), dict(tables=None), dict(lens=None), dict(ws=None),
-              dict(stride=3), dict(cols=0), dict(B=-1), dict(nq=3), dict(nq=0), dict(nq=8192), dict(window=-1), dict(scale=float("nan")),
+              dict(stride=3), dict(cols=0), dict(B=-1), dict(nq=3), dict(nq=0), dict(nq=8192), dict(B=2**30 + 1), dict(window=-1), dict(scale=float("nan")),
               dict(scale=float("inf")), dict(size=100), dict(cols=1 << 27, stride=1 << 27), dict(q=heads(None)), dict(q=heads(token=-8)),
               dict(out=heads(FAKE * 8, 256, 32)), dict(B=3, out=heads(FAKE * 8, 64, 64)), dict(out=heads(FAKE + 256)), dict(out=heads())):
         assert attn(L, **a) == -2, a

@@ -340,6 +340,22 @@ def test_attention_calls_that_overlap_on_two_streams():
         assert all(torch.equal(o, want) for o in outs)
 
 
+@pytest.mark.parametrize("B,n_q,n_kv,longest", [(127, 4, 1, 600), (128, 4, 2, 400), (129, 8, 4, 300), (1300, 4, 2, 90), (5000, 2, 1, 40)])
+@pytest.mark.parametrize("gap", [1, 5, 500])
+def test_attention_many_sequences_with_empty_stretches(B, n_q, n_kv, longest, gap):
+    """Batches around and past what a warp looks at together, most of them empty in long runs, the last among them."""
+    r = torch.Generator().manual_seed(B + gap)
+    lens = torch.randint(1, longest, (B,), generator=r)
+    lens[(torch.arange(B) // gap) % 2 == 1] = 0
+    lens[-3:] = 0
+    cache, tables, n, g = make_batch(lens.tolist(), 16, n_kv, 64, BF, "NHD", seed=B)
+    q = normal((B, n_q, 64), BF, g, 2.0)
+    out, lse = torch.full_like(q, float("nan")), torch.empty((B, n_q), device=DEV)
+    moe.moe_attention_decode(q, cache, tables, n, out, 0.125, lse=lse)
+    check_attention(q, cache, tables, n, 0.125, 0, out, lse)
+    moe.moe_cache_check()
+
+
 @pytest.mark.parametrize("B,n_q,n_kv", [(64, 8, 1), (900, 8, 4)])
 def test_attention_inputs_change_right_behind_a_call_that_cuts_no_sequence(B, n_q, n_kv):
     """Sequences of one unit each leave nothing to join: what follows still has to wait for the attention itself."""
