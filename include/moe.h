@@ -293,7 +293,7 @@ typedef struct moe_kv_cache {
   int n_layers, num_pages, page_size, n_kv;
   int head_dim;                   /* a multiple of 16, at most 512 */
   long long layer_stride, page_stride, token_stride, head_stride;
-  float k_scale, v_scale;         /* > 0 */
+  float k_scale, v_scale;         /* > 0, normal (1 / scale is finite) */
 } moe_kv_cache;
 
 /* Rows of heads: element (t, h, i) at p + t * token_stride + h * head_stride + i (elements; p

@@ -101,8 +101,8 @@ int check_cache(const moe_kv_cache *c, int layer, int dtype) {
     if (d.stride < span) return fail(MOE_ERR_BAD_ARG, "the cache's strides overlap");
     span += (d.n - 1) * d.stride;
   }
-  if (!(c->k_scale > 0) || !(c->v_scale > 0) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
-    return fail(MOE_ERR_BAD_ARG, "k_scale and v_scale must be positive and finite");
+  if (!std::isnormal(c->k_scale) || !std::isnormal(c->v_scale) || c->k_scale < 0 || c->v_scale < 0)   // 1 / scale is finite too
+    return fail(MOE_ERR_BAD_ARG, "k_scale and v_scale must be positive, normal and finite");
   if (c->dtype != MOE_DT_E4M3 && (c->k_scale != 1.f || c->v_scale != 1.f))
     return fail(MOE_ERR_BAD_ARG, "k_scale and v_scale are for 8-bit caches: 1 otherwise");
   return MOE_OK;
@@ -309,7 +309,8 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
     return fail(MOE_ERR_BAD_ARG, "max_pages = %d (rows %lld apart) of %d tokens: need 1 <= max_pages <= table_stride and at "
                                  "most 2^30 tokens", max_pages, table_stride, cache->page_size);
   if (window < 0) return fail(MOE_ERR_BAD_ARG, "window = %d < 0", window);
-  if (!std::isfinite(scale)) return fail(MOE_ERR_BAD_ARG, "scale must be finite");
+  const float scale_log2 = (float)((double)scale * cache->k_scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return fail(MOE_ERR_BAD_ARG, "scale (times k_scale, log2 e) must be finite");
   const int D = cache->head_dim, rows_b = B > 0 ? B : 1;
   rc = check_apart(out, "out", rows_b, n_q, D);
   if (rc) return rc;
@@ -347,7 +348,7 @@ int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cach
   p.num_pages = cache->num_pages;
   p.window = window;
   p.groups_of_8 = cache->page_size % 8 == 0 && p.tok_b < (1ll << 28);   // row offsets within a group in 32 bits
-  p.scale_log2 = (float)((double)scale * cache->k_scale * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   p.v_scale = cache->v_scale;
   p.out = out->p, p.out_tok = out->token_stride, p.out_head = out->head_stride;
   p.lse = lse;

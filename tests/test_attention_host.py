@@ -43,7 +43,7 @@ BAD_CACHES = [
     (dict(token_stride=64), -2),        # tokens on top of heads
     (dict(page_stride=1024), -2), (dict(layer_stride=2048), -2), (dict(head_stride=0), -2),
     (dict(k_scale=0.5), -2), (dict(dtype=moe.MOE_DT_E4M3, v_scale=0.0), -2), (dict(dtype=moe.MOE_DT_E4M3, k_scale=float("inf")), -2),
-    (dict(dtype=moe.MOE_DT_E4M3, k_scale=float("nan")), -2),
+    (dict(dtype=moe.MOE_DT_E4M3, k_scale=float("nan")), -2), (dict(dtype=moe.MOE_DT_E4M3, v_scale=1e-39), -2), (dict(dtype=moe.MOE_DT_E4M3, k_scale=-1.0), -2),
 ]
 
 
@@ -73,7 +73,7 @@ def attn(L, q=None, dt=0, c=None, layer=0, tables=FAKE, stride=4, cols=4, lens=F
 def test_attention_refusals(L):
     for a in (dict(dt=2), dict(dt=7), dict(dt=1), dict(layer=2), dict(layer=-1), dict(tables=None), dict(lens=None), dict(ws=None),
               dict(stride=3), dict(cols=0), dict(B=-1), dict(nq=3), dict(nq=0), dict(nq=8192), dict(B=2**30 + 1), dict(window=-1), dict(scale=float("nan")),
-              dict(scale=float("inf")), dict(size=100), dict(cols=1 << 27, stride=1 << 27), dict(q=heads(None)), dict(q=heads(token=-8)),
+              dict(scale=float("inf")), dict(scale=3e38), dict(size=100), dict(cols=1 << 27, stride=1 << 27), dict(q=heads(None)), dict(q=heads(token=-8)),
               dict(out=heads(FAKE * 8, 256, 32)), dict(B=3, out=heads(FAKE * 8, 64, 64)), dict(out=heads(FAKE + 256)), dict(out=heads())):
         assert attn(L, **a) == -2, a
         assert L.moe_last_error()
