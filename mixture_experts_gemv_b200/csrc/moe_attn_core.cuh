@@ -120,9 +120,14 @@ template <int W, int NT, int ES> struct Shape {
   static constexpr int kTiles = kRow <= 256 && NT <= 2 ? 2 : 1;
   static constexpr int kTok = 16 * kTiles, kLog = kTiles == 1 ? 4 : 5;   // tokens of a unit, and log2
   static constexpr int kUnit = kTok * kRow;         // bytes of its K or V rows
-  // Slots of kUnit in a warp's ring: 96 KB a CTA, two CTAs an SM (192 KB and one where a slot is
-  // 16 KB): at least 128 KB of copies in flight on an SM
-  static constexpr int kSlots = kUnit >= 16384 ? 3 : kUnit <= 4096 ? 4 : 24576 / kUnit;
+  // FP32 rows of the tile's heads, which a warp stages in its ring when its block joins its pieces
+  static constexpr int kStage = W * NT * 32;
+  // Slots of kUnit in a warp's ring, which has to hold kStage too: of 16 KB 3 (192 KB a CTA), of
+  // 8 KB 3 (96 KB), of 4 KB and less 4 (64 KB and 32 KB a CTA), or as many as kStage takes: wide
+  // groups over short rows have 8 of 2 KB, 8 or 16 of 1 KB (32 or 64 KB a CTA)
+  static constexpr int kCopySlots = kUnit >= 16384 ? 3 : kUnit <= 4096 ? 4 : 24576 / kUnit;
+  static constexpr int kSlots = kCopySlots * kUnit >= kStage ? kCopySlots : (kStage + kUnit - 1) / kUnit;
+  static_assert(kSlots * kUnit >= kStage, "a warp's ring holds its staged rows");
   static constexpr int kRows = 8 * NT;
   static constexpr int kSmem = kWarps * kSlots * kUnit;
   static constexpr int kPieces = kRow / 16;         // 16-byte pieces of a row
