@@ -41,7 +41,7 @@ struct AttnParams {
   long long out_tok, out_head;
   float *lse;                            // [B, nq] or null
   float *ws_o;                           // [2 workers][D / 16][column tiles][32 lanes][4] unnormalised sums
-  float2 *ws_ml;                         // [2 workers][rows] maximum (log2) and sum
+  float2 *ws_ml;                         // [2 workers][rows] base (log2) and sum
   int4 *ws_cut;                          // [workers] cut segments: first worker and (bit 16) whether blocks join, last worker, sequence, number there
   int noted, by_segment;                 // whether they are noted; by segment, not by the worker in which one starts
   uint32_t *err;

@@ -25,8 +25,10 @@
 //
 // Precision: K Q^T products are exact, summed in FP32; the softmax runs in FP32 (base 2); P is
 // rounded to the 16-bit type of the V product (half a step, 2^-8 or 2^-11 of each p; the sum l
-// keeps the unrounded p); O is FP32 and rounded once. fp16: p is taken times 2^15, so that
-// what fp16 cannot hold lies below 2^-39 of the largest p.
+// keeps the unrounded p); O is FP32 and rounded once. p is 2^(score - base), the base being the
+// largest score so far; for fp16 15 below it, rounded up, so that the largest p is at most 2^15 at
+// any size of the scores, and what fp16 cannot hold lies below 2^-39 of it (2^-32 where the scores'
+// own steps are 4 and more). Sums are kept with their base, so its rounding reaches no result.
 //
 // Measured (bytes of the keys in range, over the two launches replayed in a graph; a copy streams
 // 6.5 TB/s): one sequence of 997 tokens, 8 KV heads of 128 8.4 us; of 10,000, 8 of 256 21.9 us =
@@ -62,7 +64,7 @@ template <> struct Mma<__nv_bfloat16> {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);
   }
-  static constexpr float kOff = 0.f;   // log2 of the factor on p
+  static __device__ __forceinline__ float base(float top) { return top; }
 };
 template <> struct Mma<__half> {
   static __device__ __forceinline__ void run(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -74,7 +76,7 @@ template <> struct Mma<__half> {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);
   }
-  static constexpr float kOff = 15.f;
+  static __device__ __forceinline__ float base(float top) { return __fadd_ru(top, -15.f); }
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -195,7 +197,7 @@ struct Pieces {
   }
 };
 
-// Two heads' maxima and sums (m, l, m, l) and a fragment of their unnormalised rows, joined from pieces.
+// Two heads' bases and sums (m, l, m, l) and a fragment of their unnormalised rows, joined from pieces.
 struct Joined {
   float4 ml, acc;
   __device__ __forceinline__ Joined() {
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[s][n][e] = 0.f;
-    float mx[NT][2], l[NT][2];
+    float mx[NT][2], l[NT][2];   // bases (-inf: no key yet) and sums
 #pragma unroll
     for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = ninf, l[n][0] = l[n][1] = 0.f;
 
@@ -765,12 +767,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
           m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
           m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
         }
-        m0 = fmaxf(m0, mx[n][0]);
-        m1 = fmaxf(m1, mx[n][1]);
-        // a maximum of -inf (no key yet) must not meet itself in a difference
-        const float b0 = (m0 == ninf ? 0.f : m0) - M::kOff, b1 = (m1 == ninf ? 0.f : m1) - M::kOff;
-        al[n][0] = exp2_fast(mx[n][0] - M::kOff - b0);
-        al[n][1] = exp2_fast(mx[n][1] - M::kOff - b1);
+        m0 = fmaxf(M::base(m0), mx[n][0]);
+        m1 = fmaxf(M::base(m1), mx[n][1]);
+        // a base of -inf must not meet itself in a difference
+        const float b0 = m0 == ninf ? 0.f : m0, b1 = m1 == ninf ? 0.f : m1;
+        al[n][0] = exp2_fast(mx[n][0] - b0);
+        al[n][1] = exp2_fast(mx[n][1] - b1);
         scale_o |= m0 != mx[n][0] || m1 != mx[n][1];
         mx[n][0] = m0;
         mx[n][1] = m1;
@@ -864,8 +866,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
                                    make_float4(o[k][n][0], o[k][n][1], o[k][n][2], o[k][n][3]), inv0, inv1);
         if (p.lse && g == 0) {
           float *lse = p.lse + (long long)at.b * p.nq + h0 + 8 * n + 2 * c;
-          if (8 * n + 2 * c < heads) lse[0] = (mx[n][0] + (log2f(l[n][0]) - M::kOff)) * kLn2;
-          if (8 * n + 2 * c + 1 < heads) lse[1] = (mx[n][1] + (log2f(l[n][1]) - M::kOff)) * kLn2;
+          if (8 * n + 2 * c < heads) lse[0] = (mx[n][0] + log2f(l[n][0])) * kLn2;
+          if (8 * n + 2 * c + 1 < heads) lse[1] = (mx[n][1] + log2f(l[n][1])) * kLn2;
         }
       }
     } else {
@@ -928,7 +930,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
 constexpr int kJoinMost = 512;   // threads
 constexpr int kJoinPar = 16;     // groups
 template <typename TO, int ES, bool NOTED>
-__global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int log, int all_workers, int nt, int par, float off) {
+__global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int log, int all_workers, int nt, int par) {
   extern __shared__ __align__(16) float4 s_acc[];   // [threads] sums, [threads] (m, l): where par > 1
   float4 *s_ml = s_acc + blockDim.x;
   int w0, w1, b, seg;
@@ -1006,8 +1008,8 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
                          sum.ml.w == 0.f ? 0.f : p.v_scale / sum.ml.w);
   if (p.lse && k == 0 && lane < 4) {
     float *lse = p.lse + (long long)b * p.nq + h0 + 2 * c;
-    if (2 * c < heads) lse[0] = (sum.ml.x + (log2f(sum.ml.y) - off)) * kLn2;
-    if (2 * c + 1 < heads) lse[1] = (sum.ml.z + (log2f(sum.ml.w) - off)) * kLn2;
+    if (2 * c < heads) lse[0] = (sum.ml.x + log2f(sum.ml.y)) * kLn2;
+    if (2 * c + 1 < heads) lse[1] = (sum.ml.z + log2f(sum.ml.w)) * kLn2;
   }
 }
 
@@ -1038,7 +1040,7 @@ template <typename T, int W, int NT, int ES, bool QB> int launch(AttnParams p, i
   if (cudaLaunchKernelEx(&l.cfg, fn, p) != cudaSuccess) return -1;
   const int threads = par > 4 ? kJoinMost : kJoinMost / 2, frags = p.D / 16 * NT * 32, per = threads / par;
   PdlLaunch j(dim3(p.by_segment ? (unsigned)segments : workers, (frags + per - 1) / per), threads, par > 1 ? threads * 32 : 0, s);
-  if (cudaLaunchKernelEx(&j.cfg, p.noted ? k_attn_join<TO, ES, true> : k_attn_join<TO, ES, false>, p, S::kLog, workers, NT, par, Mma<T>::kOff) != cudaSuccess) return -1;
+  if (cudaLaunchKernelEx(&j.cfg, p.noted ? k_attn_join<TO, ES, true> : k_attn_join<TO, ES, false>, p, S::kLog, workers, NT, par) != cudaSuccess) return -1;
   moe_prof_count(2);
   return 0;
 }

@@ -1,0 +1,54 @@
+"""One-token attention at scores far beyond what the steps of 32-bit numbers resolve, against the 64-bit form."""
+import pytest
+import torch
+
+import mixture_experts_gemv_b200 as moe
+from test_gpu_attention import BF, DEV, E4, FP, _built, make_batch, normal  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+LN2 = 0.693147182464599609375   # ln 2 in 32 bits: times log2 e it rounds to 1, so scores in base 2 stay whole numbers
+
+
+@pytest.mark.parametrize("dtype,cache_dtype", [(BF, BF), (FP, FP), (BF, E4), (FP, E4)])
+@pytest.mark.parametrize("power", [10, 23, 24, 25, 26, 27, 28, 29, 40, 60])
+@pytest.mark.parametrize("lens,nkv,D", [([1, 40, 700, 5000], 1, 64), ([60000, 0, 33], 2, 128)])   # few units; blocks that join
+def test_scores_of_any_size(lens, nkv, D, power, dtype, cache_dtype):
+    """Scores (in base 2) of +-2^power plus a few of its steps: q . k = +-2^23 + j is exact in 32 bits, and so is its
+    product with the scale, a power of two in base 2. The probabilities are then powers of two, at any size."""
+    cache, tables, n, g = make_batch(lens, 16, nkv, D, cache_dtype, "NHD", seed=power)
+    ks, vs = (0.5, 0.25) if cache_dtype == E4 else (1.0, 1.0)
+    shape = cache.k.shape[:-1]
+    k = torch.zeros(cache.k.shape, device=DEV)
+    k[..., 0] = 256
+    k[..., 1] = torch.randint(-3, 1, shape, generator=g, device=DEV)
+    k = k.to(cache_dtype)
+    cache = moe.MoeKvCache(k, cache.v, "NHD", ks, vs)
+    nq = 6 * nkv
+    q = torch.zeros((len(lens), nq, D), device=DEV, dtype=dtype)
+    q[..., 0::2, 0], q[..., 1::2, 0] = 2.0 ** 15, -2.0 ** 15
+    q[..., 1] = 1
+    out, lse = torch.full_like(q, float("nan")), torch.full((len(lens), nq), float("nan"), device=DEV)
+    scale = LN2 * 2.0 ** (power - 23) / ks
+    moe.moe_attention_decode(q, cache, tables, n, out, scale, lse=lse)
+    moe.moe_cache_check()
+    u_o, u_p = {BF: 2.0 ** -8, FP: 2.0 ** -11}[dtype], 2.0 ** -8 if cache_dtype == BF else 2.0 ** -11
+    for b, length in enumerate(lens):
+        if length == 0:
+            assert (out[b] == 0).all() and (lse[b] == float("-inf")).all()
+            continue
+        t = torch.arange(length, device=DEV)
+        page, at = tables[b].long()[t // 16], t % 16
+        rows = [x.view(torch.uint8)[page, at].contiguous().view(cache_dtype).float().double().transpose(0, 1) * s
+                for x, s in ((k, ks), (cache.v, vs))]
+        s = (q[b].double().view(nkv, 6, D) @ rows[0].transpose(1, 2)) * scale
+        want = torch.logsumexp(s, -1, keepdim=True)
+        p = torch.softmax(s, -1)   # not exp(s - want): 64 bits do not hold s and the logarithm of a count at 2^60
+        o, size = p @ rows[1], p @ rows[1].abs()
+        # scores differ by whole numbers times the scale, which is off by 2^-28 of its value from a power of two; p and
+        # the output are rounded once each; 32-bit sums over the keys: n / 16 + 64 roundings, twice over; exp2 2^-21.
+        # Scores above the largest by 128 steps of base 2 and more leave nothing, in 32 bits as in 64.
+        rest = u_p + 2 * (length / 16 + 64) * 2.0 ** -24 + 2.0 ** -21 + 3 * 2.0 ** (min(power - 23, 8) - 28)
+        assert ((out[b].double().view(nkv, 6, D) - o).abs() <= (size * rest + u_o * o.abs()) * 1.01 + 1e-30).all()
+        # the logarithm: base plus log2 of the sum, and the product with ln 2: 4 roundings of its size
+        off = (lse[b].double().view(nkv, 6, 1) - want).abs()
+        assert (off <= 4 * 2.0 ** -24 * want.abs() + rest + 16 * 2.0 ** -23).all()
