@@ -31,7 +31,7 @@
 // own steps are 4 and more). Sums are kept with their base, so its rounding reaches no result.
 //
 // Measured (bytes of the keys in range, over the two launches replayed in a graph; a copy streams
-// 6.5 TB/s): one sequence of 997 tokens, 8 KV heads of 128 8.4 us; of 10,000, 8 of 256 21.9 us =
+// 6.5 TB/s): one sequence of 997 tokens, 8 KV heads of 128 8.7 us; of 10,000, 8 of 256 21.9 us =
 // 3.7 TB/s; of 40,000, 2 of 512 41.6 us = 3.9; 8 sequences of up to 40,000, 8 of 128 43.3 us = 4.9;
 // 128 of up to 4,096 in 8 bits, 4 of 128 48 us = 4.7; past 1 GB 5.6 to 5.9 TB/s. What does not
 // grow with the lengths is about 9 us: 1.6 until a warp knows its range, 3 to 5 until the first K
@@ -237,7 +237,7 @@ template <bool COLD> struct Numbering {
   int filled;           // sequences with a key up to there
   int next[kOwn];       // the next strip's lengths
 
-  __device__ __forceinline__ void load(const AttnParams &p, int at, int (&to)[kOwn]) const {
+  static __device__ __forceinline__ void load(const AttnParams &p, int at, int (&to)[kOwn]) {
     const int b = at + kOwn * (threadIdx.x & 31);
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
@@ -920,12 +920,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
 
 // Sums the pieces of one cut segment: segment blockIdx.x (by_segment), or the one that starts in
 // worker blockIdx.x and goes on behind it. NOTED: which workers have its pieces is what the worker
-// that starts it noted. Otherwise (few segments, by_segment) it follows from the lengths, before the
-// attention kernel's results are waited for: that kernel lets this one start only when what came
-// before it is done, so the lengths are there; they are read past L1. (Noted, calls of up to eight
-// sequences took 0.3 to 1.7 us more; numbered here, 128 sequences of 4 KV heads took 4 us more and
-// 1,024 short ones 12.) A thread takes one fragment of a piece (two heads at two elements: four values), of every par-th
-// piece: the block's threads are par groups over the same threads / par fragments. Then the
+// that starts it noted. Otherwise (few segments, by_segment) it follows from the lengths. They are
+// read and numbered while the attention kernel still runs, then read again behind the wait for it,
+// beside the pieces; only what is read there counts: where a length differs, all is done again.
+// (Noted, calls of up to eight sequences took 0.3 to 1.7 us more, the check 0.3 at 997 tokens and
+// nothing on longer ones; numbered here, 128 sequences of 4 KV heads took 4 us more and 1,024 short
+// ones 12.) A thread takes one fragment of a piece (two heads at two elements: four values), of every
+// par-th piece: the block's threads are par groups over the same threads / par fragments. Then the
 // groups' sums are joined.
 constexpr int kJoinMost = 512;   // threads
 constexpr int kJoinPar = 16;     // groups
@@ -933,53 +934,25 @@ template <typename TO, int ES, bool NOTED>
 __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__ AttnParams p, int log, int all_workers, int nt, int par) {
   extern __shared__ __align__(16) float4 s_acc[];   // [threads] sums, [threads] (m, l): where par > 1
   float4 *s_ml = s_acc + blockDim.x;
-  int w0, w1, b, seg;
-  bool joined;
-  if constexpr (NOTED) {
-    pdl_wait();
-    const int4 cut = __ldcg(p.ws_cut + blockIdx.x);
-    w0 = cut.x & 0xffff;
-    w1 = cut.y;
-    b = cut.z;
-    seg = cut.w;
-    joined = cut.x >> 16;
-  } else {
-    Numbering<true> num(p, log, all_workers);
-    b = blockIdx.x / num.segs;
-    seg = blockIdx.x - b * num.segs;
-#pragma unroll 1
-    while (b >= num.base + num.kStrip) num.next_strip(p);
-    const Numbering<true>::Segment s = num.segment(b - num.base, seg);
-    w0 = w1 = 0;
-    if (s.n) {
-      w0 = num.split.owner(s.first + num.extra);
-      w1 = num.split.owner(s.first + num.extra + s.n - 1);
-    }
-    joined = num.extra;
-  }
-  if (w1 == w0) {
-    // nothing to join. One block waits all the same: this kernel must not end, and let what follows
-    // start, before the attention kernel has ended
-    if (!NOTED && blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
-    return;
-  }
+  int w0, w1, b, h0, heads;   // heads: that exist from this column tile on
   const int tid = threadIdx.x, lane = tid & 31, per = blockDim.x / par, j0 = tid / per;   // per: a multiple of 32
   const int frags = p.D / 16 * nt * 32, f = blockIdx.y * per + (tid - j0 * per);
   const int k = f / (32 * nt), n = f / 32 - k * nt, c = lane & 3;
-  const int kvh = kv_head(p, seg), h0 = kvh * p.group + (seg - kvh * p.n_groups) * 8 * nt + 8 * n;
-  const int heads = (kvh + 1) * p.group - h0;   // that exist from this column tile on
-  const Pieces pieces(w0, w1, joined);
   const float4 *po = reinterpret_cast<const float4 *>(p.ws_o) + f, *pm = reinterpret_cast<const float4 *>(p.ws_ml) + (4 * n + c);
-  if (!NOTED) pdl_wait();
+  auto rows_of = [&](int seg) {
+    const int kvh = kv_head(p, seg);
+    h0 = kvh * p.group + (seg - kvh * p.n_groups) * 8 * nt + 8 * n;
+    heads = (kvh + 1) * p.group - h0;
+  };
   Joined sum;
-  if (f < frags) {
+  auto take = [&](const Pieces &pieces) {
+    if (f >= frags || w1 == w0) return;
     constexpr int kAhead = 4;
     for (int j = j0; j < pieces.count; j += kAhead * par) {
       float4 m[kAhead], v[kAhead];
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) {
-        const int i = j + x * par;
-        if (i >= pieces.count) continue;
+        const int i = min(j + x * par, pieces.count - 1);   // loads without a branch: all in flight together
         // piece 0: the starting worker's second slot; then the later workers' first slots
         const long long at = 2ll * pieces.worker(i) + (i == 0 ? 1 : 0);
         m[x] = pm[at * (4 * nt)];
@@ -989,6 +962,45 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
       for (int x = 0; x < kAhead; ++x)
         if (j + x * par < pieces.count) sum.take(m[x], v[x]);
     }
+  };
+  if constexpr (NOTED) {
+    pdl_wait();
+    const int4 cut = __ldcg(p.ws_cut + blockIdx.x);
+    w0 = cut.x & 0xffff;
+    w1 = cut.y;
+    if (w1 == w0) return;   // nothing to join
+    b = cut.z;
+    rows_of(cut.w);
+    take(Pieces(w0, w1, cut.x >> 16));
+  } else {
+    using Num = Numbering<true>;
+    bool other;
+    int turn = 0;
+    do {
+      const Num num(p, log, all_workers);   // its first strip has all sequences: segments are few
+      b = blockIdx.x / num.segs;
+      const int seg = blockIdx.x - b * num.segs;
+      const typename Num::Segment s = num.segment(b, seg);
+      w0 = w1 = 0;
+      if (s.n) {
+        w0 = num.split.owner(s.first + num.extra);
+        w1 = num.split.owner(s.first + num.extra + s.n - 1);
+      }
+      rows_of(seg);
+      Pieces pieces(w0, w1, num.extra);
+      // worked out in front of the wait: the compiler would move some of it behind
+      asm volatile("" : "+r"(pieces.w0), "+r"(pieces.head), "+r"(pieces.blocks), "+r"(pieces.tail), "+r"(pieces.count), "+l"(po), "+l"(pm),
+                   "+r"(h0), "+r"(heads));
+      pdl_wait();
+      int now[Num::kOwn];
+      Num::load(p, 0, now);
+      sum = Joined();
+      take(pieces);
+      other = false;
+#pragma unroll
+      for (int j = 0; j < Num::kOwn; ++j) other |= now[j] != num.len[j];
+    } while (__any_sync(Num::kAll, other) && ++turn < 2);   // the second time all is read behind the wait
+    if (w1 == w0) return;   // nothing to join
   }
   // groups of up to four join at a time: 16 -> 4 -> 1
   for (int groups = par; groups > 1; groups = (groups + 3) / 4) {
