@@ -25,7 +25,7 @@
  *  - `stream` is a cudaStream_t (0 = legacy default stream); work is enqueued on it and
  *    the call returns without synchronising;
  *  - the return value is MOE_OK (0) or a negative MOE_ERR_*; moe_last_error() then
- *    describes the failure. Argument errors are detected before anything is enqueued.
+ *    describes the failure to the thread that made the call. Argument errors are detected before anything is enqueued.
  *  - one process-wide context: calls are not thread-safe, and forwards that overlap on
  *    different streams race on the shared workspace.
  */
@@ -166,7 +166,8 @@ int moe_set_path(int path, int gemv_max_tokens);
 /* moe_destroy: synchronise the device and free the workspace. Safe to call twice. */
 void moe_destroy(void);
 
-/* moe_last_error: text for the last non-zero return of this library (static storage). */
+/* moe_last_error: text for the calling thread's last non-zero return of this library (storage of
+ * that thread). */
 const char *moe_last_error(void);
 
 /*

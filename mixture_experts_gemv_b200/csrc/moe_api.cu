@@ -1,6 +1,7 @@
 // moe_api.cu -- the C ABI (include/moe.h): context, workspace, argument checks, path
 // selection and the launches on the caller's stream. Nothing here computes the layer;
 // every step runs in the kernels of moe_route.cu, moe_gemv.cu and moe_gemm_sm100.cu.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -34,11 +35,11 @@ struct Ctx {
 };
 
 Ctx g;
-char g_err[512] = "";
+thread_local char g_err[512] = "";   // of each thread: the attention entry points may run on several
 
 // Per-kernel event timing: pairs of events recorded around each launch of a kernel group.
 struct Prof {
-  bool active = false;
+  std::atomic<bool> active{false};
   std::vector<cudaEvent_t> pool;
   size_t used = 0;
   struct Rec { int id; cudaEvent_t a, b; };
@@ -46,7 +47,7 @@ struct Prof {
   int open_id[MOE_K_COUNT];
   cudaEvent_t open_ev[MOE_K_COUNT];
   bool overflow = false;
-  long long kernels = 0;   // kernel launches since moe_profile_begin
+  std::atomic<long long> kernels{0};   // kernel launches since moe_profile_begin, of any thread
 };
 Prof g_prof;
 
@@ -262,7 +263,7 @@ void moe_prof_mark(cudaStream_t s, int id, bool begin) {
 }
 
 void moe_prof_count(int n) {
-  if (g_prof.active) g_prof.kernels += n;
+  if (g_prof.active.load(std::memory_order_relaxed)) g_prof.kernels.fetch_add(n, std::memory_order_relaxed);
 }
 
 bool moe_allow_dyn_smem(const void *fn, unsigned long long *done_mask) {
