@@ -390,8 +390,10 @@ size_t moe_attention_decode_workspace_bytes(int n_q, int n_kv, int head_dim);
 int moe_copy_pages(const moe_kv_cache *cache, const int32_t *src, const int32_t *dst, int n,
                    int32_t *block_tables, long long table_stride, int rows, int cols, void *stream);
 
-/* moe_cache_check: synchronise `stream`, then read and clear the current device's error word:
- * MOE_ERR_BAD_ARG if a call since the last check met a page, length or slot out of range. */
+/* moe_cache_check: wait for `stream`, then read and clear the current device's error word, in one step:
+ * MOE_ERR_BAD_ARG if a call met a page, length or slot out of range, of the calls that came before on
+ * `stream` or had ended on other streams, and since the last check. What a call elsewhere sets later
+ * stays for the next check. Refused while `stream` is being captured. */
 int moe_cache_check(void *stream);
 
 /* moe_workspace_bytes: device bytes moe_init would allocate for the given limits. */

@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <mutex>
+#include <thread>
 
 #include "moe_attn.cuh"
 #include "moe_pages.cuh"
@@ -20,9 +21,15 @@ namespace {
 // kept until moe_cache_check reads it.
 __device__ uint32_t g_cache_error;
 
+// Takes the error word and clears it in one step: what is set behind it stays for the next check.
+constexpr int kTaken = 32;   // checks at once
+__device__ uint32_t g_cache_taken[kTaken];
+__global__ void k_take_error(int slot) { g_cache_taken[slot] = atomicExch(&g_cache_error, 0u); }
+
 struct Device {
   std::atomic<bool> ready{false};
-  uint32_t *err = nullptr;
+  uint32_t *err = nullptr, *taken = nullptr;
+  std::atomic<uint32_t> taking{0};   // slots of `taken` that checks hold
   int num_sms = 0;
 };
 constexpr int kMaxDevices = 64;
@@ -58,6 +65,9 @@ int device(Device **out) {
       e = cudaGetSymbolAddress(&p, g_cache_error);
       if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
       d.err = static_cast<uint32_t *>(p);
+      e = cudaGetSymbolAddress(&p, g_cache_taken);
+      if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
+      d.taken = static_cast<uint32_t *>(p);
       d.num_sms = sms;
       d.ready.store(true, std::memory_order_release);
     }
@@ -440,13 +450,23 @@ int moe_cache_check(void *stream) {
   int rc = device(&dev);
   if (rc) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t v = 0;
-  cudaError_t e = cudaMemcpyAsync(&v, dev->err, sizeof v, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && v) {
-    e = cudaMemsetAsync(dev->err, 0, sizeof v, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(s, &capture);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "moe_cache_check: %s", cudaGetErrorString(e));
+  if (capture != cudaStreamCaptureStatusNone) return fail(MOE_ERR_BAD_ARG, "moe_cache_check waits for its stream: not while that is captured");
+  int slot = -1;
+  while (slot < 0) {   // a slot that no other thread's check holds
+    uint32_t held = dev->taking.load(std::memory_order_relaxed);
+    const int free_slot = ~held ? __builtin_ctz(~held) : -1;
+    if (free_slot < 0) std::this_thread::yield();
+    else if (dev->taking.compare_exchange_weak(held, held | 1u << free_slot, std::memory_order_acquire)) slot = free_slot;
   }
+  uint32_t v = 0;
+  k_take_error<<<1, 1, 0, s>>>(slot);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&v, dev->taken + slot, sizeof v, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  dev->taking.fetch_and(~(1u << slot), std::memory_order_release);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "moe_cache_check: %s", cudaGetErrorString(e));
   switch (v & 0xffffu) {
     case 0: return MOE_OK;

@@ -85,3 +85,89 @@ def test_launches_of_several_threads_are_all_counted(L):
     moe.moe_profile_end()
     moe.moe_destroy()
     assert n == 4 * 500
+
+
+@pytest.mark.gpu
+def test_no_error_is_lost_between_checks_of_two_threads(L):
+    """A check takes the error word and clears it at once: while another thread checks all the time, each error that is
+    raised here is reported, there or here."""
+    k = torch.zeros(4, 16, 1, 64, device="cuda:0", dtype=torch.bfloat16)
+    cache = moe.MoeKvCache(k, k.clone())
+    new = torch.zeros(1, 1, 64, device="cuda:0", dtype=torch.bfloat16)
+    out = torch.zeros_like(new)
+    past = torch.tensor([64], device="cuda:0")                               # a slot past the cache
+    table = torch.tensor([[9]], device="cuda:0", dtype=torch.int32)          # a page that is not there
+    one = torch.tensor([1], device="cuda:0", dtype=torch.int32)
+    ws = torch.empty(moe.moe_attention_decode_workspace_bytes(1, 1, 64), device="cuda:0", dtype=torch.uint8)
+    mine, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    moe.moe_cache_check()
+    seen, stop = {"slot": 0, "block-table": 0}, threading.Event()
+    lock = threading.Lock()
+
+    def check(stream):
+        try:
+            moe.moe_cache_check(stream=stream)
+        except moe.MoeError as e:
+            with lock:
+                for kind in seen:
+                    seen[kind] += kind in str(e)
+
+    def keep_checking():
+        while not stop.is_set():
+            check(other)
+
+    def keep_busy():   # the other stream always has about 0.2 ms of work queued, whatever the check enqueues next
+        events = []
+        with torch.cuda.stream(other):
+            while not stop.is_set():
+                torch.cuda._sleep(100000)
+                events.append(torch.cuda.Event())
+                events[-1].record()
+                if len(events) > 4:
+                    events.pop(0).synchronize()
+
+    threads = [threading.Thread(target=f) for f in (keep_busy, keep_checking)]
+    for t in threads:
+        t.start()
+    lost = 0
+    try:
+        for i in range(400):
+            kind = ("slot", "block-table")[i % 2]
+            with lock:
+                before = seen[kind]
+            if i % 2 == 0:
+                moe.moe_qk_norm_rope(None, new, new, None, None, cache=cache, slots=past, stream=mine)
+            else:
+                moe.moe_attention_decode(new, cache, table, one, out, 1.0, workspace=ws, stream=mine)
+            mine.synchronize()
+            check(mine)
+            for _ in range(200):   # the other thread may have taken it, and be on its way to count it
+                if seen[kind] != before:
+                    break
+                stop.wait(0.001)
+            lost += seen[kind] == before
+    finally:
+        stop.set()
+        for t in threads:
+            t.join()
+    assert lost == 0
+    moe.moe_cache_check()
+
+
+@pytest.mark.gpu
+def test_a_check_under_capture_is_refused_and_leaves_the_capture_whole(L):
+    k = torch.ones(4, 16, 1, 64, device="cuda:0", dtype=torch.bfloat16)
+    k[1] = 2
+    cache = moe.MoeKvCache(k, k.clone())
+    moe.moe_copy_pages(cache, [0], [2])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_copy_pages(cache, [1], [3])
+        with pytest.raises(moe.MoeError) as e:
+            moe.moe_cache_check()
+        assert "captured" in str(e.value)
+    graph.replay()
+    assert (k[3] == 2).all()
+    moe.moe_cache_check()
