@@ -373,12 +373,16 @@ template <int LOG> struct Cursor {
 };
 __device__ __forceinline__ int kv_head(const AttnParams &p, int seg) { return p.n_groups == 1 ? seg : seg / p.n_groups; }
 
-// One accumulator fragment (two heads' values at two elements, x inv) into the rows of a KV head's
-// group: out points at head 8 n, `heads` of them exist. 16 ES-dependent elements from 16 k on.
+// One accumulator fragment (two heads' values at two elements, over their sums l) into the rows of a
+// KV head's group: out points at head 8 n, `heads` of them exist. 16 ES-dependent elements from 16 k
+// on. An 8-bit cache's scale comes last: over l it could fall below the normal numbers.
 template <typename TO, int ES>
-__device__ __forceinline__ void store_fragment(TO *out, long long out_head, int k, int heads, int lane, const float4 &v, float inv0, float inv1) {
+__device__ __forceinline__ void store_fragment(TO *out, long long out_head, int k, int heads, int lane, float4 v, float l0, float l1, float v_scale) {
   const int g = lane >> 2, c = lane & 3;
-  const uint32_t lo = transposed8x8(Mma<TO>::pack(v.x * inv0, v.y * inv1)), hi = transposed8x8(Mma<TO>::pack(v.z * inv0, v.w * inv1));
+  const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
+  v = make_float4(v.x * inv0, v.y * inv1, v.z * inv0, v.w * inv1);
+  if constexpr (ES == 1) v = make_float4(v.x * v_scale, v.y * v_scale, v.z * v_scale, v.w * v_scale);
+  const uint32_t lo = transposed8x8(Mma<TO>::pack(v.x, v.y)), hi = transposed8x8(Mma<TO>::pack(v.z, v.w));
   if (g >= heads) return;
   TO *row = out + g * out_head + 16 * k;
   if constexpr (ES == 2) {   // rows g and g + 8 of the tile are elements g and g + 8
@@ -858,12 +862,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
       TO *out = static_cast<TO *>(p.out) + (long long)at.b * p.out_tok + (long long)h0 * p.out_head;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float inv0 = l[n][0] == 0.f ? 0.f : p.v_scale / l[n][0], inv1 = l[n][1] == 0.f ? 0.f : p.v_scale / l[n][1];
 #pragma unroll
         for (int k = 0; k < W / 16; ++k)
           if (16 * k < p.D)
             store_fragment<TO, ES>(out + 8 * n * p.out_head, p.out_head, k, heads - 8 * n, lane,
-                                   make_float4(o[k][n][0], o[k][n][1], o[k][n][2], o[k][n][3]), inv0, inv1);
+                                   make_float4(o[k][n][0], o[k][n][1], o[k][n][2], o[k][n][3]), l[n][0], l[n][1], p.v_scale);
         if (p.lse && g == 0) {
           float *lse = p.lse + (long long)at.b * p.nq + h0 + 8 * n + 2 * c;
           if (8 * n + 2 * c < heads) lse[0] = (mx[n][0] + log2f(l[n][0])) * kLn2;
@@ -1016,8 +1019,7 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
   if (j0) return;
   if (f - lane >= frags) return;   // whole warps
   TO *out = static_cast<TO *>(p.out) + (long long)b * p.out_tok + (long long)h0 * p.out_head;
-  store_fragment<TO, ES>(out, p.out_head, k, heads, lane, sum.acc, sum.ml.y == 0.f ? 0.f : p.v_scale / sum.ml.y,
-                         sum.ml.w == 0.f ? 0.f : p.v_scale / sum.ml.w);
+  store_fragment<TO, ES>(out, p.out_head, k, heads, lane, sum.acc, sum.ml.y, sum.ml.w, p.v_scale);
   if (p.lse && k == 0 && lane < 4) {
     float *lse = p.lse + (long long)b * p.nq + h0 + 2 * c;
     if (2 * c < heads) lse[0] = (sum.ml.x + log2f(sum.ml.y)) * kLn2;

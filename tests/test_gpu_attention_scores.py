@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import attn_ref as ref
 import mixture_experts_gemv_b200 as moe
 from test_gpu_attention import BF, DEV, E4, FP, _built, make_batch, normal  # noqa: F401
 
@@ -52,3 +53,22 @@ def test_scores_of_any_size(lens, nkv, D, power, dtype, cache_dtype):
         # the logarithm: base plus log2 of the sum, and the product with ln 2: 4 roundings of its size
         off = (lse[b].double().view(nkv, 6, 1) - want).abs()
         assert (off <= 4 * 2.0 ** -24 * want.abs() + rest + 16 * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("dtype,v_scale", [(BF, 2.0 ** -126), (BF, 1.7e-38), (BF, 2.0 ** -100), (BF, 2.0 ** 100), (FP, 2.0 ** -126),
+                                           (FP, 2.0 ** -20), (FP, 64.0)])
+@pytest.mark.parametrize("lens,nkv", [([1, 40, 700, 5000], 1), ([60000, 33], 2)])
+def test_scales_of_values_at_the_ends_of_their_range(lens, nkv, v_scale, dtype):
+    """Values of an 8-bit cache times a scale that is as small as a normal number may be, or large: outputs keep their
+    relative accuracy wherever the output's type holds them (bf16: down to 2^-126)."""
+    D, nq = 64, 6 * nkv
+    cache, tables, n, g = make_batch(lens, 16, nkv, D, E4, "NHD", seed=len(lens))
+    cache = moe.MoeKvCache(cache.k, cache.v, "NHD", 0.1, v_scale)
+    q = normal((len(lens), nq, D), dtype, g, 1.0)
+    out = torch.full_like(q, float("nan"))
+    moe.moe_attention_decode(q, cache, tables, n, out, 0.125)
+    want, _, tol, _ = ref.attention(q, cache, tables, n, 0.125)
+    assert want.abs().max() < (3e38 if dtype == BF else 65000)
+    # below its normal numbers a type rounds by half a step of its smallest ones; the bound's own 1e-30 comes off
+    tiny = 2.0 ** -134 if dtype == BF else 2.0 ** -25
+    assert ((out.double() - want).abs() <= tol - 1e-30 * 1.01 + tiny).all()
