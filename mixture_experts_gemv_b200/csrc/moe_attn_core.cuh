@@ -23,7 +23,8 @@
 // joins its warps' first), and the join kernel, launched behind with programmatic dependent
 // launch, sums them in order. No atomics: outputs repeat bit for bit.
 //
-// Precision: K Q^T products are exact, summed in FP32; the softmax runs in FP32 (base 2); P is
+// Precision: K Q^T products are exact (of a bf16 q over an 8-bit cache, for elements from 2^-31 of the
+// head's largest on), summed in FP32; the softmax runs in FP32 (base 2); P is
 // rounded to the 16-bit type of the V product (half a step, 2^-8 or 2^-11 of each p; the sum l
 // keeps the unrounded p); O is FP32 and rounded once. p is 2^(score - base), the base being the
 // largest score so far; for fp16 15 below it, rounded up, so that the largest p is at most 2^15 at
@@ -626,9 +627,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
           sc[n][0] = sc[n][1] = p.scale_log2;
         } else {
           // k index of the e4m3 fragments: b0 holds elements 4c, 4c + 1 of the 16, b1 4c + 2, 4c + 3.
-          // q is scaled by a power of two that puts the head's largest value in [1, 2), so that
-          // fp16 holds a bf16 q; the scores are multiplied back.
-          float top = 0.f;
+          // An fp16 q is taken as it is. A bf16 one is multiplied by a power of two that puts the
+          // head's largest value in [2^14, 2^15), so that fp16 holds it: exactly from 2^-31 of that
+          // value on, smaller elements to 2^-39 of it. The scores are multiplied back.
           uint2 raw[W / 16];
 #pragma unroll
           for (int s = 0; s < W / 16; ++s) {
@@ -636,39 +637,42 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_decode(const __grid_consta
             raw[s] = make_uint2(0u, 0u);
             if (hh < heads && d < p.D) raw[s] = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.q) + q_at + d);
           }
-          auto up = [&](uint32_t w, float &x, float &y) {
-            if constexpr (QB) {
+          if constexpr (QB) {
+            auto up = [](uint32_t w, float &x, float &y) {
               x = __uint_as_float(w << 16);
               y = __uint_as_float(w & 0xffff0000u);
-            } else {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-              x = f.x;
-              y = f.y;
+            };
+            float top = 0.f;
+#pragma unroll
+            for (int s = 0; s < W / 16; ++s) {
+              float x, y;
+              up(raw[s].x, x, y);
+              top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+              up(raw[s].y, x, y);
+              top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
             }
-          };
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+            const int eb = max((int)(__float_as_uint(top) >> 23), 15);   // biased exponent; both factors are normal
+            const float down = __uint_as_float((uint32_t)(268 - eb) << 23), back = __uint_as_float((uint32_t)(eb - 14) << 23);
 #pragma unroll
-          for (int s = 0; s < W / 16; ++s) {
-            float x, y;
-            up(raw[s].x, x, y);
-            top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
-            up(raw[s].y, x, y);
-            top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
-          }
-          top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-          int eb = (int)(__float_as_uint(top) >> 23);          // biased exponent
-          eb = eb < 1 ? 127 : (eb > 253 ? 253 : eb);
-          const float down = __uint_as_float((uint32_t)(254 - eb) << 23), back = __uint_as_float((uint32_t)eb << 23);
+            for (int s = 0; s < W / 16; ++s) {
+              float x, y;
+              up(raw[s].x, x, y);
+              qf[s][n][0] = M::pack(x * down, y * down);
+              up(raw[s].y, x, y);
+              qf[s][n][1] = M::pack(x * down, y * down);
+            }
+            sc[n][0] = p.scale_log2 * __shfl_sync(kAll, back, 8 * c);
+            sc[n][1] = p.scale_log2 * __shfl_sync(kAll, back, 8 * c + 4);
+          } else {
 #pragma unroll
-          for (int s = 0; s < W / 16; ++s) {
-            float x, y;
-            up(raw[s].x, x, y);
-            qf[s][n][0] = M::pack(x * down, y * down);
-            up(raw[s].y, x, y);
-            qf[s][n][1] = M::pack(x * down, y * down);
+            for (int s = 0; s < W / 16; ++s) {
+              qf[s][n][0] = raw[s].x;
+              qf[s][n][1] = raw[s].y;
+            }
+            sc[n][0] = sc[n][1] = p.scale_log2;
           }
-          sc[n][0] = p.scale_log2 * __shfl_sync(kAll, back, 8 * c);
-          sc[n][1] = p.scale_log2 * __shfl_sync(kAll, back, 8 * c + 4);
         }
       }
     };

@@ -4,7 +4,7 @@ import torch
 
 import attn_ref as ref
 import mixture_experts_gemv_b200 as moe
-from test_gpu_attention import BF, DEV, E4, FP, _built, make_batch, normal  # noqa: F401
+from test_gpu_attention import BF, DEV, E4, FP, _built, check_attention, make_batch, normal  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 LN2 = 0.693147182464599609375   # ln 2 in 32 bits: times log2 e it rounds to 1, so scores in base 2 stay whole numbers
@@ -72,3 +72,33 @@ def test_scales_of_values_at_the_ends_of_their_range(lens, nkv, v_scale, dtype):
     # below its normal numbers a type rounds by half a step of its smallest ones; the bound's own 1e-30 comes off
     tiny = 2.0 ** -134 if dtype == BF else 2.0 ** -25
     assert ((out.double() - want).abs() <= tol - 1e-30 * 1.01 + tiny).all()
+
+
+@pytest.mark.parametrize("dtype,large,small,scale", [(BF, 2.0 ** 10, 2.0 ** -10, 2.0 ** 9), (BF, 2.0 ** 100, 2.0 ** 72, 2.0 ** -73), (FP, 60000.0, 2.0 ** -8, 2.0 ** 7),
+                                                     (BF, 2.0 ** -110, 2.0 ** -126, 2.0 ** 125)])
+@pytest.mark.parametrize("lens,nkv", [([1, 40, 700], 1), ([60000, 33], 2)])
+def test_queries_of_very_different_elements_over_8_bits(lens, nkv, dtype, large, small, scale):
+    """One element of q is 2^16 to 2^28 times the others and meets zeros: the scores come from the others alone, whose bits
+    all count. fp16 queries are taken as they are. Of a bf16 head, whose largest element becomes 2^14 or more in fp16,
+    an element is off by at most half a step of fp16's smallest numbers, 2^-25: 2^-39 of the largest."""
+    D, nq = 64, 6 * nkv
+    cache, tables, n, g = make_batch(lens, 16, nkv, D, E4, "NHD", seed=len(lens))
+    cache.k.view(torch.uint8)[..., 5] = 0
+    q = normal((len(lens), nq, D), torch.float32, g, 1.0).clamp(-3.9, 3.9) * small
+    q = q.to(dtype)
+    q[..., 5] = large
+    out, lse = torch.full_like(q, float("nan")), torch.full((len(lens), nq), float("nan"), device=DEV)
+    moe.moe_attention_decode(q, cache, tables, n, out, scale, lse=lse)
+    if dtype == FP:
+        check_attention(q, cache, tables, n, scale, 0, out, lse)
+        return
+    want, want_lse, tol, lse_tol = ref.attention(q, cache, tables, n, scale)
+    size = ref.attention(q, moe.MoeKvCache(cache.k, (cache.v.view(torch.uint8) & 127).view(E4), "NHD", cache.k_scale, cache.v_scale),
+                         tables, n, scale)[0]   # sum of p |v|
+    for b, length in enumerate(lens):
+        t = torch.arange(length, device=DEV)
+        k = ref.cache_rows(cache, 0, "k", tables[b].long()[t // 16], t % 16).abs().sum(-1).amax(0)   # [nkv]
+        moved = scale * 2.0 ** -39 * q[b].double().abs().amax(-1) * k.repeat_interleave(6)   # of each score
+        # p moves by twice that (its score and the sum), the logarithm of the sum by as much
+        assert ((out[b].double() - want[b]).abs() <= tol[b] + 2.02 * moved[:, None] * size[b]).all()
+        assert ((lse[b].double() - want_lse[b]).abs() <= lse_tol[b] + moved).all()
