@@ -320,7 +320,8 @@ typedef struct moe_heads {
  *   q_gain, k_gain  device fp32 [head_dim], 16-byte aligned, or NULL for no norm
  *   q_out, k_out    where rotated q and k go, type dtype; NULL leaves k_out out (q_out only
  *               where n_q = 0). Each may be its own input (same base and strides), and none may
- *               overlap anything else that the call reads or writes.
+ *               overlap anything else that the call reads or writes. Parts of one buffer's rows may lie
+ *               between each other, head by head too, where their token strides are equal.
  *   cache, layer, slots  NULL, or the cache that k (rotated) and v are stored in: token t in row
  *               slots[t] % page_size of page slots[t] / page_size (device int64 [T]; negative:
  *               not stored). Its dtype is dtype or MOE_DT_E4M3 (value times 1 / scale in FP32, saturated at

@@ -140,16 +140,30 @@ bool same(const moe_heads *a, const moe_heads *b) {
   return a->p == b->p && a->token_stride == b->token_stride && a->head_stride == b->head_stride;
 }
 
-// Whether rows of T tokens of nx and of ny heads (2-byte elements) share an address.
+// Whether rows of T tokens of nx and of ny heads (2-byte elements) share an address. Rows of unlike
+// token strides, and more than 2^16 pairs of heads, count as sharing one where their extents do.
 bool overlap(const moe_heads *x, int nx, const moe_heads *y, int ny, int T, int D) {
-  const long long wx = 2 * ((nx - 1) * x->head_stride + D), wy = 2 * ((ny - 1) * y->head_stride + D);   // a token's span
+  const long long row = 2ll * D, hx = 2 * x->head_stride, hy = 2 * y->head_stride;   // bytes
+  const long long wx = (nx - 1) * hx + row, wy = (ny - 1) * hy + row;                // a token's span
   const uintptr_t ax = reinterpret_cast<uintptr_t>(x->p), ay = reinterpret_cast<uintptr_t>(y->p);
   const uintptr_t bx = ax + 2 * (uintptr_t)(T - 1) * x->token_stride + wx, by = ay + 2 * (uintptr_t)(T - 1) * y->token_stride + wy;
   if (ax >= by || ay >= bx) return false;
-  // parts of the rows of one buffer: apart when the spans are, modulo a token
-  if (x->token_stride != y->token_stride || x->token_stride == 0) return true;
-  const long long step = 2 * x->token_stride, gap = (((long long)(ay - ax)) % step + step) % step;
-  return gap < wx || gap + wy > step;
+  const long long step = T > 1 ? 2 * x->token_stride : 0, apart = (long long)(ay - ax);
+  if (T > 1 && x->token_stride != y->token_stride) return true;
+  if (step) {   // parts of the rows of one buffer: apart when the spans are, modulo a token
+    const long long gap = (apart % step + step) % step;
+    if (gap >= wx && gap + wy <= step) return false;
+  }
+  if ((long long)nx * ny > 1 << 16) return true;
+  // heads between each other's heads: every pair, at the tokens that bring it closest
+  for (int i = 0; i < nx; ++i)
+    for (int j = 0; j < ny; ++j) {
+      const long long d = apart + j * hy - i * hx;   // from x's row to y's, of one token
+      const long long t = step ? std::min<long long>(std::max<long long>(-d / step, 1 - T), T - 1) : 0;
+      for (long long u = std::max<long long>(t - 1, 1 - T); u <= std::min<long long>(t + 1, T - 1); ++u)
+        if (std::llabs(d + u * step) < row) return true;
+    }
+  return false;
 }
 
 bool mult_of(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
