@@ -298,16 +298,18 @@ def moe_debug_inject(fault: int) -> None:
 
 _torch = None        # torch and the codes of its types, at the first call
 _dtype_codes = None
-_raw_stream = None
+_raw_stream = None   # device -> the handle of its current stream
+_device = None       # () -> the current device
 
 
 def _setup():
-    global _torch, _dtype_codes, _raw_stream
+    global _torch, _dtype_codes, _raw_stream, _device
     import torch
     _dtype_codes = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float8_e4m3fn: MOE_DT_E4M3}
     # the current stream's handle without a Stream object around it
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
 
 
@@ -351,7 +353,7 @@ def _call(fn, index, stream, *args):
         stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if _torch._C._cuda_getDevice() == index:
+    if _device() == index:
         rc = fn(*args, stream)
     else:
         with _torch.cuda.device(index):

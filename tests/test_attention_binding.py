@@ -1,0 +1,21 @@
+"""The binding of the attention operators where torch lacks the private functions that save it host time."""
+import torch
+
+from mixture_experts_gemv_b200 import _lib
+
+
+def test_the_binding_does_without_torchs_private_functions(monkeypatch):
+    kept = {name: getattr(_lib, name) for name in ("_torch", "_dtype_codes", "_raw_stream", "_device")}
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    for name, value in kept.items():
+        monkeypatch.setattr(_lib, name, value)   # put back afterwards
+    _lib._setup()
+    assert _lib._device is torch.cuda.current_device
+    asked = []
+    monkeypatch.setattr(_lib, "_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: asked.append(index) or torch.cuda.ExternalStream)
+    monkeypatch.setattr(torch.cuda.ExternalStream, "cuda_stream", 77, raising=False)
+    got = []
+    _lib._call(lambda *a: got.append(a) or _lib.MOE_OK, 3, None, 1, 2)
+    assert got == [(1, 2, 77)] and asked == [3]
