@@ -1031,7 +1031,8 @@ __global__ void __launch_bounds__(kJoinMost) k_attn_join(const __grid_constant__
   }
 }
 
-template <typename T, int W, int NT, int ES, bool QB> int launch(AttnParams p, int num_sms, cudaStream_t s) {
+// static: what it keeps is this copy of the library's (a process may load several, each with its kernels)
+template <typename T, int W, int NT, int ES, bool QB> static int launch(AttnParams p, int num_sms, cudaStream_t s) {
   using S = Shape<W, NT, ES>;
   using TO = std::conditional_t<ES == 1 && QB, __nv_bfloat16, T>;
   static unsigned long long attr_done = 0;
@@ -1063,7 +1064,7 @@ template <typename T, int W, int NT, int ES, bool QB> int launch(AttnParams p, i
   return 0;
 }
 
-template <typename T, int ES, bool QB> int dispatch(const AttnParams &p, int num_sms, cudaStream_t s) {
+template <typename T, int ES, bool QB> static int dispatch(const AttnParams &p, int num_sms, cudaStream_t s) {
   const int nt = moe_attn_tiles(p.D, p.group);
   switch (moe_attn_width(p.D)) {
     case 64:

@@ -1,4 +1,6 @@
 """The binding of the attention operators where torch lacks the private functions that save it host time."""
+import subprocess
+
 import torch
 
 from mixture_experts_gemv_b200 import _lib
@@ -19,3 +21,12 @@ def test_the_binding_does_without_torchs_private_functions(monkeypatch):
     got = []
     _lib._call(lambda *a: got.append(a) or _lib.MOE_OK, 3, None, 1, 2)
     assert got == [(1, 2, 77)] and asked == [3]
+
+
+def test_the_library_shares_no_variable_with_another_copy_of_itself():
+    """A variable that the linker makes one of a kind in the process would be shared by a second copy of the library,
+    whose kernels are its own."""
+    from mixture_experts_gemv_b200 import build
+    names = subprocess.run(["nm", "-D", build.build()], check=True, capture_output=True, text=True).stdout
+    unique = [line for line in names.splitlines() if line.split()[-2:-1] == ["u"]]
+    assert "moe_attention_decode" in names and not unique, unique[:5]
