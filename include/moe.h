@@ -365,12 +365,15 @@ int moe_rope_frequencies(int kind, int rotary_dim, double base, double factor, d
  *                i * page_size ... of a sequence. Entries past a sequence's end are not read.
  *   seq_lens     device int32 [B], keys per sequence. Length 0, and a sequence whose scores are
  *                all -inf, gives a row of zeros and lse = -inf.
- *   out          [B, n_q, head_dim] of q's type, apart from q;  lse device fp32 [B, n_q] or NULL
+ *   out          [B, n_q, head_dim] of q's type;  lse device fp32 [B, n_q] or NULL. out, lse and
+ *                workspace share nothing with each other or with what is read (out on q is refused)
  *   workspace    device, moe_attention_decode_workspace_bytes(...) bytes, 16-byte aligned; needs no
  *                initial contents and keeps nothing between calls
  * Limits: max_pages * page_size <= 2^30, B <= 2^30, n_q <= 4096. Two launches on `stream`. Deterministic: the work split
- * follows from the lengths alone and pieces are summed in order. Softmax in FP32; the
- * probabilities are rounded to 16 bits (bf16 for a bf16 cache, else fp16) for the product with v.
+ * follows from the lengths alone and pieces are summed in order. Products q . k in FP32 (a bf16 q over
+ * an 8-bit cache: elements below 2^-31 of their head's largest count to 2^-39 of it); softmax in
+ * FP32; the probabilities are rounded to 16 bits (bf16 for a bf16 cache, else fp16, to 2^-40 of the
+ * largest one) for the product with v.
  */
 int moe_attention_decode(const moe_heads *q, int dtype, const moe_kv_cache *cache, int layer,
                          const int32_t *block_tables, long long table_stride, int max_pages,

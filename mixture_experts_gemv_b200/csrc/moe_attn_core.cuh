@@ -23,22 +23,28 @@
 // joins its warps' first), and the join kernel, launched behind with programmatic dependent
 // launch, sums them in order. No atomics: outputs repeat bit for bit.
 //
-// Precision: K Q^T products are exact (of a bf16 q over an 8-bit cache, for elements from 2^-31 of the
-// head's largest on), summed in FP32; the softmax runs in FP32 (base 2); P is
-// rounded to the 16-bit type of the V product (half a step, 2^-8 or 2^-11 of each p; the sum l
-// keeps the unrounded p); O is FP32 and rounded once. p is 2^(score - base), the base being the
-// largest score so far; for fp16 15 below it, rounded up, so that the largest p is at most 2^15 at
-// any size of the scores, and what fp16 cannot hold lies below 2^-39 of it (2^-32 where the scores'
-// own steps are 4 and more). Sums are kept with their base, so its rounding reaches no result.
+// Precision: K Q^T products are exact (of a bf16 q over an 8-bit cache, for elements from 2^-31 of
+// the head's largest on), summed in FP32; the softmax runs in FP32 (base 2); P is rounded to the
+// 16-bit type of the V product (half a step, 2^-8 or 2^-11 of each p; the sum l keeps the unrounded
+// p); O is FP32 and rounded once. p is 2^(score - base), the base being the largest score so far; for
+// fp16 15 below it, rounded up, so that the largest p is at most 2^15 at any size of the scores, and
+// what fp16 cannot hold lies below 2^-39 of it (2^-32 where the scores' own steps are 4 and more).
+// Sums are kept with their base, so its rounding reaches no result.
 //
 // Measured (bytes of the keys in range, over the two launches replayed in a graph; a copy streams
 // 6.5 TB/s): one sequence of 997 tokens, 8 KV heads of 128 8.7 us; of 10,000, 8 of 256 21.9 us =
-// 3.7 TB/s; of 40,000, 2 of 512 41.6 us = 3.9; 8 sequences of up to 40,000, 8 of 128 43.3 us = 4.9;
-// 128 of up to 4,096 in 8 bits, 4 of 128 48 us = 4.7; past 1 GB 5.6 to 5.9 TB/s. What does not
-// grow with the lengths is about 9 us: 1.6 until a warp knows its range, 3 to 5 until the first K
-// rows are there, 1 for the blocks' pieces, 3 for the join; and 0.01 us a sequence, for the
-// numbering: 1,024 sequences of 64 tokens of one KV head take 15 us. 8-bit caches are bound by
-// instructions, the conversions to fp16 among them.
+// 3.7 TB/s; of 40,000, 2 of 512 41.8 us = 3.9; 8 sequences of up to 40,000, 8 of 128 43.8 us = 4.8;
+// 128 of up to 4,096 in 8 bits, 4 of 128 48.6 us = 4.7; 64 of 16,384, 8 of 128 (4.3 GB) 626 us = 6.9.
+// What does not grow with the lengths is about 9 us: 1.6 until a warp knows its range, 3 to 5 until
+// the first K rows are there, 1 for the blocks' pieces, 3 for the join; and 0.01 us a sequence, for
+// the numbering: 1,024 sequences of 64 tokens of one KV head take 15.6 us, out of L2. Over 8-bit
+// caches neither memory (64 %) nor issue (41 %) is busy: 12 warps an SM wait for their own chain of
+// conversions, products and softmax.
+//
+// Wide groups and wide heads hold more than 255 registers: heads of 512 spill 200 to 320 bytes a
+// thread, 16 query heads of 256 260 to 600, 32 of 128 400 to 660, 64 of 64 810 to 1,200. Their time is
+// the warp's own work: 8 sequences of 40,000 with 71 query heads on one KV head of 64 take 176 us, with
+// 32 on one of 128 in 8 bits 80 us; the bytes are 12.5 us in both.
 //
 // Tried and left: K's 8-bit products as they are, q in two or three 8-bit terms (mma.sync with 8-bit
 // operands is emulated: the 8-bit case went from 59 to 67 us); one bulk copy a row (a warp issues

@@ -12,10 +12,10 @@
 // and angles are folded into four factors a pair that stay in registers. With few tokens a token's
 // heads are spread over several warps so that the GPU is filled. V = 4 up to head_dim 256 (8-byte
 // pieces, 64 registers, 32 warps an SM, the next two passes' loads in flight), V = 8 above (a head
-// would not fit a warp; 80 registers, 24 warps).
+// would not fit a warp; 80 registers, 24 warps). Both bounds cost 24 to 80 bytes of spills a thread.
 //
 // Measured (4,096 tokens of 32 + 8 + 8 heads of 128, bf16, 101 MB; 10,000 of 16 + 2 + 2 heads of
-// 512 into an 8-bit cache, 389 MB): 26.1 and 83.8 us = 3.9 and 4.6 TB/s; without norm and rotation
+// 512 into an 8-bit cache, 389 MB): 25.4 and 83.4 us = 4.0 and 4.7 TB/s; without norm and rotation
 // the first takes 22.9 us, a plain copy of the bytes 17.4. Tried: V = 8 with 24 warps 30.9 us, one
 // load ahead 28.0, three 26.3; rows through shared memory by cp.async rings four or eight deep
 // 30.8 and 39.7 (more instructions); by bulk copies with a warp of their own and three stages 24.5 to
