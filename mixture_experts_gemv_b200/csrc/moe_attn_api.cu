@@ -478,6 +478,7 @@ int moe_cache_check(void *stream) {
   uint32_t v = 0;
   k_take_error<<<1, 1, 0, s>>>(slot);
   e = cudaGetLastError();
+  if (e == cudaSuccess) moe_prof_count(1);
   if (e == cudaSuccess) e = cudaMemcpyAsync(&v, dev->taken + slot, sizeof v, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   dev->taking.fetch_and(~(1u << slot), std::memory_order_release);

@@ -81,10 +81,11 @@ def test_launches_of_several_threads_are_all_counted(L):
     for t in all_:
         t.join()
     n = moe.moe_profile_kernel_launches()
-    torch.cuda.synchronize()
+    moe.moe_cache_check()   # one kernel too
+    with_check = moe.moe_profile_kernel_launches()
     moe.moe_profile_end()
     moe.moe_destroy()
-    assert n == 4 * 500
+    assert n == 4 * 500 and with_check == n + 1
 
 
 @pytest.mark.gpu
